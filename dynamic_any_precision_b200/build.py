@@ -37,6 +37,9 @@ CU_SOURCES = {
     "stack_glue.cu": [],
     "probe.cu": [],
     "rates.cu": ["--fmad=false"],
+    "pairs.cu": [],
+    "linear_tc.cu": [],
+    "dense_abi.cu": [],
 }
 CPP_SOURCES = {"encode.cpp": ["-O2", "-ffp-contract=off", "-fno-fast-math"]}
 

@@ -224,4 +224,63 @@ cudaError_t launch_shared(const SharedArgs& a, cudaStream_t stream);
 cudaError_t launch_residual_rmsnorm(const uint16_t* y, float* h, uint16_t* x, int T, int H, float eps,
                                     cudaStream_t stream);
 
+// Routed pairs sorted by expert, and the rows that travel with them (pairs.cu).
+constexpr int kSortMaxExperts = 1024;
+struct SortArgs {
+    const int32_t* idx;       // [P] expert of each pair; outside [0, E): not routed
+    int P, E;
+    int32_t* pos;             // [P] place of each pair, -1 if not routed
+    int32_t* order;           // [P] pair at each place, unrouted pairs last
+    int32_t* offsets;         // [E + 1] places before each expert
+    int32_t* hist;            // [chunks][E + 1] workspace (several chunks only)
+    int chunk;                // pairs per CTA (set by the launcher)
+};
+int sort_chunk_pairs(int P);
+size_t sort_hist_bytes(int P, int E);
+cudaError_t launch_sort_pairs(const SortArgs& a, cudaStream_t stream);
+
+cudaError_t launch_permute_pairs(int elem_bytes, const void* x, const int32_t* pos, int T, int K, int H, void* out,
+                                 cudaStream_t stream, int sms);
+
+struct UnpermuteArgs {
+    const void* z;            // [T*K][H] rows by place
+    const int32_t* pos;       // [T][K]
+    const void* weights;      // [T][K] fp32 or fp64, or nullptr (all 1)
+    int wtype;                // DPA_DTYPE_FP32, DPA_DTYPE_FP64, or -1 without weights
+    const void* residual;     // [T][H] in y's type, or nullptr
+    void* y;                  // [T][H]
+    int T, K, H;
+};
+cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, cudaStream_t stream);
+
+struct UnpermuteBwdArgs {
+    const void* dy;           // [T][H]
+    const void* z;            // [T*K][H]
+    const int32_t* pos;       // [T][K]
+    const void* weights;      // [T][K] fp32 or fp64
+    int wtype;
+    void* dz;                 // [T*K][H], rows without a pair are left as they were
+    float* dweights;          // [T][K], 0 for unrouted pairs
+    int T, K, H;
+};
+cudaError_t launch_unpermute_bwd(const UnpermuteBwdArgs& a, int type, cudaStream_t stream);
+
+// Matrix products with a fused epilogue, plain or grouped by expert (linear_tc.cu).
+struct LinearArgs {
+    int rows, K, N;           // rows of x, in and out features
+    int E;                    // groups (0: plain)
+    const int32_t* offsets;   // [E + 1] first row of each group
+    const void* bias;         // [N] or [E][N], or nullptr
+    const void* bias_mul;     // the same for the second product, or nullptr
+    const void* residual;     // [rows][N] in the output's type, or nullptr
+    void* out;                // [rows][N]
+    int act, out32;           // DPA_ACT_*; 1: fp32 output
+    WsHeader* hdr;
+    // set by the launcher: K steps, feature tiles, most tokens per tile, CTAs sharing K, pipeline
+    // stages, rows per token load
+    int ksteps, FT, TN, splits, stages, xbox;
+};
+cudaError_t launch_linear(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
+                          cudaStream_t stream, int sms);
+
 }  // namespace dpa

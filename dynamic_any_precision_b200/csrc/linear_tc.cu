@@ -1,0 +1,661 @@
+// Matrix products with a fused epilogue on the fifth-generation tensor cores, plain or grouped by
+// expert:
+//     y[r] = act(W x[r] + b) [* (U x[r] + c)] [+ residual[r]]
+// x [rows][K] and the weights [N][K] (grouped: [E][N][K], rows offsets[e] .. offsets[e+1] take
+// expert e's) are bf16 or fp16; products are summed in fp32 in tensor memory (TMEM), the epilogue
+// runs in fp32, and y is rounded once (bf16, fp16) or stored as fp32.
+//
+// Orientation: the MMA's M = weight rows (128 per CTA), N = the tile's tokens, so an output
+// feature is a TMEM lane: its bias is a per-thread constant, few tokens cost few MMA columns, and
+// a warp's stores of one token are 32 consecutive features. With a gate (U given) a CTA holds 64
+// features: each 32-lane quadrant has 16 rows of W and the same 16 rows of U, so that the product
+// of both pairs lane t with lane t ^ 16 of one warp.
+//
+// Variants:
+//   CG = 2  two CTAs share one tile (256 weight rows x up to 256 tokens, cta_group::2): each loads
+//           its 128 weight rows and half of the tokens, so a 64-wide K step moves 32 KB per SM for
+//           512 cycles of MMA. For compute-bound sizes; persistent, one pair per two SMs.
+//   CG = 1  one CTA per tile of 128 weight rows x up to 128 tokens. For weight-bound sizes. With
+//           few tiles, a cluster of S CTAs splits K: every CTA leaves its partial sums in shared
+//           memory, and each then adds up its share of the outputs over the cluster, in rank
+//           order (deterministic), before the epilogue.
+//
+// Roles (320 threads): warps 0-7 epilogue (two per TMEM lane quadrant), warp 8 TMA loads (no
+// multicast), warp 9 TMEM allocation and MMA issue. Two accumulators of 256 columns alternate, so
+// a tile's epilogue overlaps the next tile's MMAs. Every wait is bounded: on a timeout the kernel
+// records DPA_ERR_DEVICE_TIMEOUT and every role leaves its loop.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc.cuh"
+
+namespace dpa {
+namespace {
+
+constexpr int kRowsA = 128;                      // weight rows per CTA (TMEM lanes)
+constexpr int kStepK = 64;                       // K per stage: one 128-byte swizzle row of 16-bit values
+constexpr int kATile = kRowsA * 128;             // 16 KB
+constexpr int kEpiWarps = 8;
+constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+constexpr int kThreads = (kEpiWarps + 2) * 32;   // 320
+constexpr int kMaxStages = 12;
+constexpr uint32_t kTmemCols = 512, kAccCols = 256;
+constexpr int kSmemMax = 232448;
+// full[stages], empty[stages], acc_full[2], acc_empty[2], done; then the TMEM address and abort flag
+constexpr int kBarBytes = (2 * kMaxStages + 5) * 8 + 16;
+
+struct Tile {
+    int e, row0, n, ft;
+};
+
+// Rows of one token tile when n rows are cut into tiles of at most tn: equal parts rounded up to
+// `step` rows.
+__host__ __device__ __forceinline__ int balanced_rows(int n, int tn, int step) {
+    const int nt = (n + tn - 1) / tn;
+    return nt == 0 ? step : ((n + nt - 1) / nt + step - 1) / step * step;
+}
+
+__device__ __forceinline__ int group_edge(const LinearArgs& a, int e) {
+    return min(max(__ldg(a.offsets + e), 0), a.rows);   // an edge outside the rows reads as the nearest row
+}
+
+template <int CG>
+__device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref, int tile) {
+    Tile t;
+    int tt = tile / a.FT;
+    t.ft = tile - tt * a.FT;
+    t.e = 0;
+    int begin = 0, n = a.rows;
+    if (a.E > 0) {   // the last group whose first token tile is not after tt
+        int lo = 0, hi = a.E - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_pref[mid] <= tt) lo = mid;
+            else hi = mid - 1;
+        }
+        t.e = lo;
+        tt -= s_pref[lo];
+        begin = group_edge(a, lo);
+        n = group_edge(a, lo + 1) - begin;
+    }
+    const int sz = balanced_rows(n, a.TN, 16 * CG);
+    t.row0 = begin + tt * sz;
+    t.n = min(n - tt * sz, sz);
+    return t;
+}
+
+// ---- epilogue arithmetic (fp32) ----
+// gelu: v Phi(v) = v erfc(-v / sqrt 2) / 2, without cancellation for negative v. gelu_tanh:
+// v (1 + tanh p) / 2 = v / (1 + exp(-2p)), p = sqrt(2/pi) (v + 0.044715 v^3).
+__device__ __forceinline__ float act_one(float v, int act) {
+    switch (act) {
+        case DPA_ACT_RELU: return v < 0.f ? 0.f : v;   // NaN stays NaN
+        case DPA_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
+        case DPA_ACT_GELU_TANH: return v / (1.f + expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+        case DPA_ACT_SILU: return v / (1.f + expf(-v));
+        default: return v;
+    }
+}
+
+template <int CNT>
+__device__ __forceinline__ void act_many(float (&v)[CNT], int act) {
+    switch (act) {   // one branch for the whole array
+        case DPA_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[j] = act_one(v[j], DPA_ACT_RELU);
+            break;
+        case DPA_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[j] = act_one(v[j], DPA_ACT_GELU);
+            break;
+        case DPA_ACT_GELU_TANH:
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[j] = act_one(v[j], DPA_ACT_GELU_TANH);
+            break;
+        case DPA_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[j] = act_one(v[j], DPA_ACT_SILU);
+            break;
+        default: break;
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ float up16(uint16_t b) {
+    if constexpr (F16) return __half2float(__ushort_as_half(b));
+    else return bf16_bits_to_float(b);
+}
+template <bool F16>
+__device__ __forceinline__ uint16_t down16(float v) {
+    if constexpr (F16) return __half_as_ushort(__float2half_rn(v));
+    else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+template <bool F16>
+__device__ __forceinline__ float bias_at(const void* b, int64_t i) {
+    return b ? up16<F16>(__ldg(static_cast<const uint16_t*>(b) + i)) : 0.f;
+}
+
+// Adds the residual (all loads first: out may be the residual itself) and stores CNT values of one
+// feature, tokens `step` apart, the first n of them.
+template <bool F16, int CNT>
+__device__ __forceinline__ void store_column(const LinearArgs& a, float (&v)[CNT], int64_t at, int64_t stride, int n) {
+    if (a.out32) {
+        const float* res = static_cast<const float*>(a.residual);
+        if (res) {
+            float r[CNT];
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) r[j] = j < n ? res[at + j * stride] : 0.f;
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[j] += r[j];
+        }
+        float* out = static_cast<float*>(a.out);
+#pragma unroll
+        for (int j = 0; j < CNT; ++j)
+            if (j < n) out[at + j * stride] = v[j];
+    } else {
+        const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+        if (res) {
+            uint16_t r[CNT];
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) r[j] = j < n ? res[at + j * stride] : static_cast<uint16_t>(0);
+#pragma unroll
+            for (int j = 0; j < CNT; ++j) v[j] += up16<F16>(r[j]);
+        }
+        uint16_t* out = static_cast<uint16_t*>(a.out);
+#pragma unroll
+        for (int j = 0; j < CNT; ++j)
+            if (j < n) out[at + j * stride] = down16<F16>(v[j]);
+    }
+}
+
+// ---- pair (cta_group::2) forms of the tensor-core operations ----
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    if constexpr (CG == 1) {
+        tc_mma(d, ad, bd, idesc, acc);
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+            : "memory");
+    }
+}
+// arrival on the same barrier of every CTA of the tile
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (CG == 1) {
+        tc_commit(bar);
+    } else {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    }
+}
+// tensor loads into this CTA's shared memory, completing on `bar` (shared::cluster address; of the
+// pair's first CTA with CG = 2)
+template <int CG>
+__device__ __forceinline__ void load2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int CG, bool GATED, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const __grid_constant__ CUtensorMap wmap,
+                                                             const __grid_constant__ CUtensorMap umap,
+                                                             const __grid_constant__ CUtensorMap xmap) {
+    constexpr int kFeat = GATED ? 64 : 128;   // output features per CTA
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+    const int stages = a.stages, btile = (a.TN / CG) * 128;
+    unsigned char* sA = sm;
+    unsigned char* sB = sm + stages * kATile;
+    unsigned char* tail = sB + stages * btile;
+    uint64_t* full = reinterpret_cast<uint64_t*>(tail);
+    uint64_t* empty = full + kMaxStages;
+    uint64_t* acc_full = empty + kMaxStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* done = acc_empty + 2;
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(done + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    int* s_pref = reinterpret_cast<int*>(tail + kBarBytes);   // [E + 1] token tiles before each group
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = a.splits;                                     // CTAs sharing K (CG = 1)
+    const int rank = CG == 2 || S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int csize = CG == 2 ? 2 : S;
+    const int cid = static_cast<int>(blockIdx.x) / csize, ncl = static_cast<int>(gridDim.x) / csize;
+
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kEpiWarps * CG);
+        }
+        mbar_init(done, 1);
+        *s_abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        if constexpr (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(const_cast<uint32_t*>(s_tmem))),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(const_cast<uint32_t*>(s_tmem))),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
+    }
+    pdl_wait();
+    // token tiles before each group (one warp; the others wait at the barrier below)
+    if (a.E > 0 && warp == kLoadWarp) {
+        int before = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int c = 0;
+            if (e < a.E) {
+                const int n = group_edge(a, e + 1) - group_edge(a, e);
+                if (n > 0) {
+                    const int sz = balanced_rows(n, a.TN, 16 * CG);
+                    c = (n + sz - 1) / sz;
+                }
+            }
+            int incl = c;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (e < a.E) s_pref[e] = before + incl - c;
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) s_pref[a.E] = before;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();   // the pair's barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const int ttiles = a.E > 0 ? s_pref[a.E] : (a.rows + a.TN - 1) / a.TN;
+    int64_t ntiles = static_cast<int64_t>(ttiles) * a.FT;
+    if (S > 1 && ntiles > ncl) ntiles = ncl;   // one tile per cluster (only offsets out of order name more)
+    // this CTA's K steps
+    const int k0 = CG == 1 ? static_cast<int>(static_cast<int64_t>(a.ksteps) * rank / S) : 0;
+    const int k1 = CG == 1 ? static_cast<int>(static_cast<int64_t>(a.ksteps) * (rank + 1) / S) : a.ksteps;
+
+    if (warp == kLoadWarp) {
+        // ================= loads: one lane =================
+        if (lane == 0) {
+            int s = 0, ph = 1;
+            bool ok = true;
+            for (int64_t it = cid; it < ntiles && ok; it += ncl) {
+                const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
+                const int part = ((t.n + 16 * CG - 1) / (16 * CG)) * 16;   // token rows of this CTA
+                const int nbox = (part + a.xbox - 1) / a.xbox;
+                const int f0 = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat;
+                const int r0 = t.row0 + (CG == 2 ? rank * part : 0);
+                const uint32_t bytes = static_cast<uint32_t>(CG) * (kATile + nbox * a.xbox * 128);
+                for (int kc = k0; kc < k1; ++kc) {
+                    if (!mbar_wait_abortable(&empty[s], ph, s_abort, a.hdr, 0x710)) {
+                        ok = false;
+                        break;
+                    }
+                    uint32_t bar = smem_u32(&full[s]);
+                    if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                    if (CG == 2) bar = mapa_shared(bar, 0);
+                    unsigned char* da = sA + s * kATile;
+                    if constexpr (GATED) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            load3d<CG>(da + q * 4096, &wmap, kc * kStepK, f0 + q * 16, t.e, bar);
+                            load3d<CG>(da + q * 4096 + 2048, &umap, kc * kStepK, f0 + q * 16, t.e, bar);
+                        }
+                    } else {
+                        load3d<CG>(da, &wmap, kc * kStepK, f0, t.e, bar);
+                    }
+                    unsigned char* db = sB + s * btile;
+                    for (int i = 0; i < nbox; ++i)
+                        load2d<CG>(db + i * a.xbox * 128, &xmap, kc * kStepK, r0 + i * a.xbox, bar);
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (*s_abort) {   // copies already issued land well within this time
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 2000000ull) __nanosleep(10000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ================= MMA issue (the pair's first CTA) =================
+        if (CG == 1 || rank == 0) {
+            const bool leader = elect_one();
+            const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB);
+            const uint64_t dconst = smem_desc_sw128(0);
+            int s = 0, ph = 0, j = 0;
+            bool ok = true;
+            for (int64_t it = cid; it < ntiles && ok; it += ncl, ++j) {
+                const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
+                const int b = j & 1;
+                const int ncols = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
+                const uint32_t idesc = instr_desc(F16 ? 0 : 1, ncols, 128 * CG);
+                const uint32_t td = tmem + static_cast<uint32_t>(b) * kAccCols;
+                bool w_ok = mbar_wait_abortable(&acc_empty[b], ((j >> 1) & 1) ^ 1, s_abort, a.hdr, 0x720);
+                if (!__all_sync(0xffffffffu, w_ok)) break;
+                for (int kc = k0; kc < k1; ++kc) {
+                    w_ok = mbar_wait_abortable(&full[s], ph, s_abort, a.hdr, 0x721);
+                    if (!__all_sync(0xffffffffu, w_ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = dconst | ((a_base + static_cast<uint32_t>(s) * kATile) >> 4);
+                    const uint64_t bd = dconst | ((b_base + static_cast<uint32_t>(s * btile)) >> 4);
+                    if (leader) {
+                        mma_f16<CG>(td, ad, bd, idesc, kc > k0 ? 1u : 0u);
+                        mma_f16<CG>(td, ad + 2, bd + 2, idesc, 1u);
+                        mma_f16<CG>(td, ad + 4, bd + 4, idesc, 1u);
+                        mma_f16<CG>(td, ad + 6, bd + 6, idesc, 1u);
+                        commit<CG>(&empty[s]);
+                        if (kc == k1 - 1) commit<CG>(&acc_full[b]);
+                    }
+                    __syncwarp();
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            // every MMA issued has completed before TMEM is released
+            if (leader) commit<CG>(done);
+            __syncwarp();
+            mbar_wait_bounded(done, 0, a.hdr, 0x722);
+            __syncwarp();
+        }
+    } else {
+        // ================= epilogue =================
+        const int q = warp & 3, half = warp >> 2, R = 32 * q + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+        uint32_t empty_bar[2] = {smem_u32(&acc_empty[0]), smem_u32(&acc_empty[1])};
+        if (CG == 2) {
+            empty_bar[0] = mapa_shared(empty_bar[0], 0);
+            empty_bar[1] = mapa_shared(empty_bar[1], 0);
+        }
+        int j = 0;
+        for (int64_t it = cid; it < ntiles; it += ncl, ++j) {
+            const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
+            const int b = j & 1;
+            const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + (GATED ? q * 16 + (lane & 15) : R);
+            const bool f_ok = f < a.N;
+            const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
+            const float bias = f_ok ? bias_at<F16>(a.bias, fb) : 0.f;
+            const float bmul = GATED && f_ok ? bias_at<F16>(a.bias_mul, fb) : 0.f;
+            const bool w_ok = mbar_wait_abortable(&acc_full[b], (j >> 1) & 1, s_abort, a.hdr, 0x730);
+            if (!__all_sync(0xffffffffu, w_ok)) break;   // tcgen05.ld below is .sync.aligned
+            tc_fence_after();
+            const int nch = (t.n + 31) >> 5;
+            const uint32_t acc = tmem + lane_base + static_cast<uint32_t>(b) * kAccCols;
+            if (CG == 1 && S > 1) {
+                // partial sums [token][128] into the (now idle) stage memory
+                float* part = reinterpret_cast<float*>(sm);
+                for (int c = half; c < nch; c += 2) {
+                    uint32_t v[32];
+                    tmem_ld32(acc + 32 * c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 32; ++u)
+                        if (32 * c + u < t.n) part[(32 * c + u) * kRowsA + R] = __uint_as_float(v[u]);
+                }
+                break;   // one tile per cluster
+            }
+            for (int c = half; c < nch; c += 2) {
+                uint32_t v[32];
+                tmem_ld32(acc + 32 * c, v);
+                tmem_wait_ld();
+                if (c + 2 >= nch) {   // last read of this accumulator by this warp
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2) arrive_cluster(empty_bar[b]);
+                        else mbarrier_arrive(&acc_empty[b]);
+                    }
+                }
+                const int tok0 = 32 * c;
+                if constexpr (GATED) {
+                    // one exchange per token pair: the W lane gets the U value of the even token, the
+                    // U lane the W value of the odd one
+                    const bool wl = (lane & 16) == 0;
+                    float g[16], m[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                        const float ev = __uint_as_float(v[2 * u]), od = __uint_as_float(v[2 * u + 1]);
+                        const float got = __shfl_xor_sync(0xffffffffu, wl ? od : ev, 16);
+                        g[u] = (wl ? ev : got) + bias;
+                        m[u] = (wl ? got : od) + bmul;
+                    }
+                    act_many(g, a.act);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) g[u] *= m[u];
+                    const int first = tok0 + (wl ? 0 : 1);
+                    if (f_ok)
+                        store_column<F16>(a, g, (static_cast<int64_t>(t.row0) + first) * a.N + f,
+                                          2 * static_cast<int64_t>(a.N), (t.n - first + 1) / 2);
+                } else {
+                    float o[32];
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) o[u] = __uint_as_float(v[u]) + bias;
+                    act_many(o, a.act);
+                    if (f_ok)
+                        store_column<F16>(a, o, (static_cast<int64_t>(t.row0) + tok0) * a.N + f, a.N, t.n - tok0);
+                }
+            }
+            if (half >= nch) {   // this warp had nothing to read
+                if (lane == 0) {
+                    if (CG == 2) arrive_cluster(empty_bar[b]);
+                    else mbarrier_arrive(&acc_empty[b]);
+                }
+            }
+        }
+    }
+    __syncwarp();
+
+    if (CG == 1 && S > 1) {
+        cluster_sync();   // every CTA's partial sums are written
+        if (cid < ntiles) {
+            const Tile t = find_tile<CG>(a, s_pref, cid);
+            const int f0 = t.ft * kFeat, tot = t.n * kFeat;
+            const int i1 = static_cast<int>(static_cast<int64_t>(tot) * (rank + 1) / S);
+            const uint32_t base = smem_u32(sm);
+            uint32_t peer[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) peer[r] = mapa_shared(base, r < S ? r : 0);
+            for (int i = static_cast<int>(static_cast<int64_t>(tot) * rank / S) + tid; i < i1; i += kThreads) {
+                const int tok = i / kFeat, fi = i - tok * kFeat, f = f0 + fi;
+                if (f >= a.N) continue;
+                const uint32_t off =
+                    static_cast<uint32_t>(tok * kRowsA + (GATED ? (fi >> 4) * 32 + (fi & 15) : fi)) * 4;
+                float pv[8], pm[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    pv[r] = r < S ? ld_cluster_f32(peer[r] + off) : 0.f;
+                    pm[r] = GATED && r < S ? ld_cluster_f32(peer[r] + off + 64) : 0.f;
+                }
+                float v = pv[0], m = pm[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r) {
+                    v += pv[r];
+                    m += pm[r];
+                }
+                const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
+                float o[1] = {act_one(v + bias_at<F16>(a.bias, fb), a.act)};
+                if (GATED) o[0] *= m + bias_at<F16>(a.bias_mul, fb);
+                store_column<F16>(a, o, (static_cast<int64_t>(t.row0) + tok) * a.N + f, 0, 1);
+            }
+        }
+        cluster_sync();   // no CTA leaves while another reads its partial sums
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync();   // both CTAs are done with the pair's barriers and TMEM
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        if constexpr (CG == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// 16-bit [groups][rows][cols] tensor, boxes of 64 columns x box_rows, 128-byte swizzle, zero fill
+bool encode_map(CUtensorMap* map, const void* base, bool f16, uint64_t cols, uint64_t rows, uint64_t groups,
+                uint32_t box_rows, int rank) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {cols, rows, groups};
+    const cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+    const cuuint32_t box[3] = {kStepK, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG, bool GATED, bool F16>
+cudaError_t launch_variant(LinearArgs& a, const CUtensorMap* maps, int clusters, size_t smem, cudaStream_t stream) {
+    const void* fn = reinterpret_cast<const void*>(linear_kernel<CG, GATED, F16>);
+    const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (err != cudaSuccess) return err;
+    const int csize = CG == 2 ? 2 : a.splits;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters) * csize);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(csize);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = csize > 1 ? 2 : 1;
+    alignas(64) CUtensorMap m0 = maps[0], m1 = maps[1], m2 = maps[2];
+    void* args[] = {&a, &m0, &m1, &m2};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const void* w, const void* w_mul,
+                          cudaStream_t stream, int sms) {
+    LinearArgs a = in;
+    const bool gated = w_mul != nullptr;
+    const int feat = gated ? 64 : 128;   // output features per CTA
+    a.ksteps = (a.K - 1) / kStepK + 1;
+    const int mean = a.E > 0 ? (a.rows - 1) / a.E + 1 : a.rows;   // rows per group
+    const int groups = a.E > 0 ? a.E : 1;
+    // a pair of CTAs per tile where tiles of 256 tokens are reasonably full and fill half the SMs
+    const int64_t pair_tiles = static_cast<int64_t>(groups) * ((mean - 1) / 256 + 1) * ((a.N - 1) / (2 * feat) + 1);
+    const bool pair = mean >= 64 && pair_tiles >= sms / 4;
+    const int CG = pair ? 2 : 1;
+    a.FT = (a.N - 1) / (feat * CG) + 1;
+    a.splits = 1;
+    int64_t clusters;
+    if (a.E > 0) {
+        a.TN = pair ? 256 : 128;
+        a.xbox = mean >= 32 ? 32 : 16;
+        // most token tiles there can be: every full tile, and one more per non-empty group
+        const int64_t tiles =
+            (static_cast<int64_t>(a.rows) / a.TN + (a.rows < a.E ? a.rows : a.E)) * a.FT;
+        if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+        if (!pair)
+            while (a.splits < 8 && a.splits < a.ksteps && tiles * (a.splits + 1) <= sms) ++a.splits;
+        clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
+    } else {
+        a.TN = balanced_rows(a.rows, pair ? 256 : 128, 16 * CG);
+        a.xbox = a.TN / CG;
+        const int64_t tiles = static_cast<int64_t>((a.rows - 1) / a.TN + 1) * a.FT;
+        if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+        if (!pair)
+            while (a.splits < 8 && a.splits < a.ksteps && tiles * (a.splits + 1) <= sms) ++a.splits;
+        clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
+    }
+    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + kBarBytes + (a.E + 1) * 4;
+    a.stages = (kSmemMax - fixed) / stage;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    const size_t smem = static_cast<size_t>(a.stages) * stage + fixed;
+    alignas(64) CUtensorMap maps[3];
+    const uint64_t E = static_cast<uint64_t>(groups);
+    const uint32_t wbox = gated ? 16 : 128;
+    if (!encode_map(&maps[0], w, f16, a.K, a.N, E, wbox, 3) ||
+        !encode_map(&maps[1], gated ? w_mul : w, f16, a.K, a.N, E, wbox, 3) ||
+        !encode_map(&maps[2], x, f16, a.K, a.rows, 1, static_cast<uint32_t>(a.xbox), 2))
+        return cudaErrorInvalidValue;
+    const int c = static_cast<int>(clusters);
+    if (pair) {
+        if (gated) return f16 ? launch_variant<2, true, true>(a, maps, c, smem, stream)
+                              : launch_variant<2, true, false>(a, maps, c, smem, stream);
+        return f16 ? launch_variant<2, false, true>(a, maps, c, smem, stream)
+                   : launch_variant<2, false, false>(a, maps, c, smem, stream);
+    }
+    if (gated) return f16 ? launch_variant<1, true, true>(a, maps, c, smem, stream)
+                          : launch_variant<1, true, false>(a, maps, c, smem, stream);
+    return f16 ? launch_variant<1, false, true>(a, maps, c, smem, stream)
+               : launch_variant<1, false, false>(a, maps, c, smem, stream);
+}
+
+}  // namespace dpa

@@ -49,6 +49,11 @@ class LayerWeights(ctypes.Structure):
                 ("expert_width", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p)]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("rows", "in_features", "out_features", "dtype", "out_dtype", "act")]
+
+
 class Aux(ctypes.Structure):
     _fields_ = [("topk_idx", ctypes.c_void_p), ("topk_gate", ctypes.c_void_p), ("k", ctypes.c_void_p),
                 ("lambda_", ctypes.c_void_p), ("pair_out", ctypes.c_void_p),
@@ -57,13 +62,19 @@ class Aux(ctypes.Structure):
 
 PATH_AUTO, PATH_GEMV, PATH_TC = 0, 1, 2
 ALLOC_LAGRANGE, ALLOC_UNIFORM, ALLOC_THRESHOLD, ALLOC_EXPERT_TABLE = 0, 1, 2, 3
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32, DTYPE_FP64 = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+LINEAR_WORKSPACE_BYTES = 256
 
 
 EXPORTED = ("dpa_encoded_sizes", "dpa_encode", "dpa_export_codes", "dpa_export_meta", "dpa_route",
             "dpa_allocate", "dpa_allocate_ex", "dpa_calibrate_threshold", "dpa_forward_workspace_size",
             "dpa_moe_forward", "dpa_device_status", "dpa_status_string", "dpa_version", "dpa_residual_rmsnorm",
             "dpa_debug_timeout_probe", "dpa_distortion_tensor", "dpa_profile_prefill", "dpa_solve_expert_rates",
-            "dpa_stream_prefixes", "dpa_solve_stored_widths", "dpa_compact_sizes", "dpa_compact_layer")
+            "dpa_stream_prefixes", "dpa_solve_stored_widths", "dpa_compact_sizes", "dpa_compact_layer",
+            "dpa_sort_workspace_size", "dpa_sort_pairs", "dpa_permute_rows", "dpa_unpermute_rows",
+            "dpa_unpermute_rows_backward", "dpa_linear", "dpa_grouped_linear")
 
 _lib = None
 
@@ -100,11 +111,19 @@ def lib() -> ctypes.CDLL:
     L.dpa_solve_stored_widths.argtypes = [P(LayerDesc), vp, vp, ctypes.c_int64, vp]
     L.dpa_compact_sizes.argtypes = [P(LayerDesc), vp, P(ctypes.c_uint64), P(ctypes.c_uint64)]
     L.dpa_compact_layer.argtypes = [P(LayerDesc), vp, vp, vp, vp, vp, vp]
+    L.dpa_sort_workspace_size.argtypes = [i32, i32]
+    L.dpa_sort_workspace_size.restype = sz
+    L.dpa_sort_pairs.argtypes = [vp, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.dpa_permute_rows.argtypes = [i32, vp, vp, i32, i32, i32, vp, vp]
+    L.dpa_unpermute_rows.argtypes = [i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, vp, vp]
+    L.dpa_unpermute_rows_backward.argtypes = [i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+    L.dpa_linear.argtypes = [P(LinearDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.dpa_grouped_linear.argtypes = [P(LinearDesc), i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.dpa_status_string.argtypes = [i32]
     L.dpa_status_string.restype = ctypes.c_char_p
     L.dpa_version.argtypes = []
     for name in EXPORTED:
-        if name not in ("dpa_forward_workspace_size", "dpa_status_string", "dpa_version"):
+        if name not in ("dpa_forward_workspace_size", "dpa_sort_workspace_size", "dpa_status_string", "dpa_version"):
             getattr(L, name).restype = i32
     L.dpa_version.restype = i32
     _lib = L
@@ -343,6 +362,223 @@ def residual_rmsnorm(h, x, y=None, stream=None):
     T, H = h.shape
     _check(lib().dpa_residual_rmsnorm(_dptr(y), _dptr(h), T, H, _dptr(x), _stream(stream)), "dpa_residual_rmsnorm")
     return x
+
+
+# ------------------------------------------------------------- dense experts: rows and products
+
+def _dtype(t) -> int:
+    """DTYPE_* of a tensor's elements (int16 and uint16 tensors hold bf16 bit patterns)."""
+    import torch
+    code = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.uint16: DTYPE_BF16,
+            torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32, torch.float64: DTYPE_FP64}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported element type {t.dtype}")
+    return code
+
+
+def _expect(t, name: str, shape, dtype=None, like=None):
+    """Check a tensor argument: shape, element type (a torch dtype or a DTYPE_* code), device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and (_dtype(t) if isinstance(dtype, int) else t.dtype) != dtype:
+        raise ValueError(f"{name}: unexpected element type {t.dtype}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: expected a tensor on {like.device}, got {t.device}")
+
+
+class _On:
+    """The device of a tensor made current for one call, and the stream of the call on it: the
+    given stream, or that device's current one."""
+
+    def __init__(self, t, stream):
+        import torch
+        if not t.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        self.device, self.stream = t.device.index, stream
+        self.other = torch.cuda.current_device() != self.device
+
+    def __enter__(self) -> int:
+        import torch
+        if self.other:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.other:
+            self.guard.__exit__(*exc)
+
+
+def sort_workspace_size(n_pairs: int, n_experts: int) -> int:
+    n = lib().dpa_sort_workspace_size(n_pairs, n_experts)
+    if n == 0:
+        raise DpaError(1, "dpa_sort_workspace_size")
+    return n
+
+
+def new_sort_workspace(n_pairs: int, n_experts: int, device=None):
+    """Zero-filled workspace for sort_pairs of up to n_pairs pairs (serves linear and
+    grouped_linear too)."""
+    import torch
+    return torch.zeros(sort_workspace_size(n_pairs, n_experts), dtype=torch.uint8, device=device or "cuda")
+
+
+def new_linear_workspace(device=None):
+    """Zero-filled workspace for linear and grouped_linear: it holds the device error flag only
+    (device_status reads it), so any workspace of the library serves as well."""
+    import torch
+    return torch.zeros(LINEAR_WORKSPACE_BYTES, dtype=torch.uint8, device=device or "cuda")
+
+
+def sort_pairs(idx, n_experts: int, ws, pos=None, order=None, offsets=None, stream=None):
+    """Stable sort of routed pairs by expert. idx: CUDA int32, any shape (one expert id per pair;
+    ids outside [0, n_experts) are not routed). Returns (pos in idx's shape, order [P], offsets
+    [n_experts + 1]), int32: the place of each pair (-1 if not routed), the pair at each place
+    (unrouted ones last), the places before each expert."""
+    import torch
+    P = idx.numel()
+    _expect(idx, "idx", idx.shape, torch.int32)
+    _expect(ws, "ws", ws.shape, torch.uint8, like=idx)
+    if pos is None:
+        pos = torch.empty_like(idx)
+    if order is None:
+        order = torch.empty(P, dtype=torch.int32, device=idx.device)
+    if offsets is None:
+        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=idx.device)
+    _expect(pos, "pos", idx.shape, torch.int32, like=idx)
+    _expect(order, "order", (P,), torch.int32, like=idx)
+    _expect(offsets, "offsets", (n_experts + 1,), torch.int32, like=idx)
+    with _On(idx, stream) as s:
+        _check(lib().dpa_sort_pairs(_dptr(idx), P, n_experts, _dptr(pos), _dptr(order), _dptr(offsets), _dptr(ws),
+                                    ws.numel(), s), "dpa_sort_pairs")
+    return pos, order, offsets
+
+
+def permute_rows(x, pos, out=None, stream=None):
+    """out[pos[t][k]] = x[t]. x: [T][H] bf16 (or int16 bits), fp16 or fp32; pos: int32 [T][K] from
+    sort_pairs. Returns out [T*K][H]; rows that no pair takes are left as they were (with out=None:
+    uninitialised)."""
+    import torch
+    T, H = x.shape
+    K = pos.shape[-1]
+    _expect(pos, "pos", (T, K), torch.int32, like=x)
+    if out is None:
+        out = torch.empty((T * K, H), dtype=x.dtype, device=x.device)
+    _expect(out, "out", (T * K, H), _dtype(x), like=x)
+    with _On(x, stream) as s:
+        _check(lib().dpa_permute_rows(_dtype(x), _dptr(x), _dptr(pos), T, K, H, _dptr(out), s), "dpa_permute_rows")
+    return out
+
+
+def permute_rows_backward(dout, pos, dx=None, stream=None):
+    """Gradient of permute_rows: dx[t] = sum_k dout[pos[t][k]] (fp32 sums, rounded once)."""
+    return unpermute_rows(dout, pos, None, out=dx, stream=stream)
+
+
+def unpermute_rows(z, pos, weights=None, residual=None, out=None, out_dtype=None, stream=None):
+    """y[t] = residual[t] + sum_k weights[t][k] * z[pos[t][k]]. z: [T*K][H]; pos: int32 [T][K];
+    weights: fp32 or fp64 [T][K] (None: all 1); residual: [T][H] of y's type, may be `out`. y has
+    out_dtype (default: residual's, else z's): z's own type, or one of the two is fp32."""
+    import torch
+    T, K = pos.shape
+    P, H = z.shape
+    _expect(pos, "pos", (T, K), torch.int32, like=z)
+    _expect(z, "z", (T * K, H))
+    if out is None:
+        dt = out_dtype or (z.dtype if residual is None else residual.dtype)
+        out = torch.empty((T, H), dtype=dt, device=z.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: unexpected element type {out.dtype}")
+    _expect(out, "out", (T, H), like=z)
+    if residual is not None:
+        _expect(residual, "residual", (T, H), _dtype(out), like=z)
+    if weights is not None:
+        _expect(weights, "weights", (T, K), like=z)
+    with _On(z, stream) as s:
+        _check(lib().dpa_unpermute_rows(_dtype(z), _dptr(z), _dptr(pos), _dptr(weights),
+                                        -1 if weights is None else _dtype(weights), _dptr(residual), _dtype(out), T,
+                                        K, H, _dptr(out), s), "dpa_unpermute_rows")
+    return out
+
+
+def unpermute_rows_backward(dy, z, pos, weights, dz=None, dweights=None, stream=None):
+    """Gradients of unpermute_rows: (dz [T*K][H] in z's type, dweights fp32 [T][K]). dy: [T][H] of
+    z's type. Rows of dz that no pair takes are left as they were (with dz=None: uninitialised);
+    pairs that are not routed get dweights 0. The residual's gradient is dy itself."""
+    import torch
+    T, K = pos.shape
+    P, H = z.shape
+    _expect(pos, "pos", (T, K), torch.int32, like=z)
+    _expect(z, "z", (T * K, H))
+    _expect(dy, "dy", (T, H), _dtype(z), like=z)
+    _expect(weights, "weights", (T, K), like=z)
+    if dz is None:
+        dz = torch.empty_like(z)
+    if dweights is None:
+        dweights = torch.empty((T, K), dtype=torch.float32, device=z.device)
+    _expect(dz, "dz", (T * K, H), _dtype(z), like=z)
+    _expect(dweights, "dweights", (T, K), torch.float32, like=z)
+    with _On(z, stream) as s:
+        _check(lib().dpa_unpermute_rows_backward(_dtype(z), _dptr(dy), _dptr(z), _dptr(pos), _dptr(weights),
+                                                 _dtype(weights), T, K, H, _dptr(dz), _dptr(dweights), s),
+               "dpa_unpermute_rows_backward")
+    return dz, dweights
+
+
+def _product(call, name, x, w, lead, ws, bias, act, w_mul, bias_mul, residual, out, out_dtype, stream):
+    """Shared argument handling of linear and grouped_linear; `lead` is () or (n_groups,)."""
+    import torch
+    rows, K = x.shape
+    N = w.shape[-2]
+    dt = _dtype(x)
+    _expect(w, "w", (*lead, N, K), dt, like=x)
+    for t, what, shape in ((bias, "bias", (*lead, N)), (w_mul, "w_mul", (*lead, N, K)),
+                           (bias_mul, "bias_mul", (*lead, N))):
+        if t is not None:
+            _expect(t, what, shape, dt, like=x)
+    if out is None:
+        odt = out_dtype or (x.dtype if residual is None else residual.dtype)
+        out = torch.empty((rows, N), dtype=odt, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: unexpected element type {out.dtype}")
+    _expect(out, "out", (rows, N), like=x)
+    if residual is not None:
+        _expect(residual, "residual", (rows, N), _dtype(out), like=x)
+    _expect(ws, "ws", ws.shape, torch.uint8, like=x)
+    if act not in ACTS:
+        raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
+    desc = LinearDesc(rows, K, N, dt, _dtype(out), ACTS[act])
+    with _On(x, stream) as s:
+        _check(call(desc, _dptr(bias), _dptr(w_mul), _dptr(bias_mul), _dptr(residual), _dptr(out), s), name)
+    return out
+
+
+def linear(x, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=None, out=None, out_dtype=None,
+           stream=None):
+    """out = act(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual]. x: [M][K] bf16 (or int16
+    bits) or fp16, K a multiple of 8; w, w_mul: [N][K]; bias, bias_mul: [N], all of x's type; out and
+    residual: [M][N] in x's type or fp32 (out_dtype; default: residual's, else x's); residual may be
+    `out`. act: "none", "relu", "gelu", "gelu_tanh" or "silu". ws: new_linear_workspace or any
+    other workspace; it receives the device error flag."""
+    return _product(lambda d, b, u, c, r, o, s: lib().dpa_linear(ctypes.byref(d), _dptr(x), _dptr(w), b, u, c, r, o,
+                                                                 _dptr(ws), ws.numel(), s),
+                    "dpa_linear", x, w, (), ws, bias, act, w_mul, bias_mul, residual, out, out_dtype, stream)
+
+
+def grouped_linear(x, offsets, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=None, out=None,
+                   out_dtype=None, stream=None):
+    """linear of each group's rows with that group's weights: rows offsets[e] .. offsets[e+1] - 1
+    take w[e]. offsets: int32 [E + 1] on the device (sort_pairs); w, w_mul: [E][N][K]; bias,
+    bias_mul: [E][N]. Rows behind offsets[E] are neither used nor written (with out=None:
+    uninitialised)."""
+    import torch
+    E = w.shape[0]
+    _expect(offsets, "offsets", (E + 1,), torch.int32, like=x)
+    return _product(lambda d, b, u, c, r, o, s: lib().dpa_grouped_linear(ctypes.byref(d), E, _dptr(x), _dptr(offsets),
+                                                                         _dptr(w), b, u, c, r, o, _dptr(ws),
+                                                                         ws.numel(), s),
+                    "dpa_grouped_linear", x, w, (E,), ws, bias, act, w_mul, bias_mul, residual, out, out_dtype, stream)
 
 
 def stream_prefixes(desc: LayerDesc, host_planes, host_meta, experts, kplanes, dev_planes, dev_meta,

@@ -429,6 +429,83 @@ dpa_status dpa_compact_layer(const dpa_layer_desc* desc, const void* planes, con
  * byte 256 of ws. ws: device, 16-byte aligned, at least 512 bytes. */
 dpa_status dpa_debug_timeout_probe(void* ws, size_t ws_bytes, int kind, uint64_t limit_ns, void* stream);
 
+/* ---- Dense experts: rows sorted by expert and back, and matrix products ----
+ * The layer at full precision, around the same router: the pairs of a batch sorted by expert, the
+ * tokens' rows brought into that order, products of each expert's rows with its weights, and the
+ * weighted sum back to the tokens. (The pages compare quantised layers with the unquantised one;
+ * they print no interface for either.) Element types of rows, weights and gates: */
+enum { DPA_DTYPE_BF16 = 0, DPA_DTYPE_FP16 = 1, DPA_DTYPE_FP32 = 2, DPA_DTYPE_FP64 = 3 };
+enum { DPA_ACT_NONE = 0, DPA_ACT_RELU = 1, DPA_ACT_GELU = 2, DPA_ACT_GELU_TANH = 3, DPA_ACT_SILU = 4 };
+
+/* Bytes of workspace dpa_sort_pairs needs for up to n_pairs pairs (0 if the sizes are invalid). The workspace is
+ * zero-filled once by the caller; calls that share one must be ordered on the device (one stream,
+ * or events), as must graphs captured with it. */
+size_t dpa_sort_workspace_size(int n_pairs, int n_experts);
+
+/* Stable sort of routed pairs by expert (device). idx: int32 [n_pairs], the expert of each pair
+ * (pair t*top_k + k is slot k of token t); an id outside [0, n_experts) marks a pair that is not
+ * routed here (padding, an expert held elsewhere). Written:
+ *   order    int32 [n_pairs]: the pair at each place, experts in ascending order, pairs of one
+ *            expert in ascending order, unrouted pairs last;
+ *   pos      int32 [n_pairs]: the place of each pair, -1 if it is not routed;
+ *   offsets  int32 [n_experts + 1]: places before each expert; offsets[n_experts] = routed pairs.
+ * Whole numbers, the same in every run. n_experts <= 1024, n_pairs <= 2^30. */
+dpa_status dpa_sort_pairs(const int32_t* idx, int n_pairs, int n_experts, int32_t* pos, int32_t* order,
+                          int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
+
+/* out[pos[t][k]] = x[t] (device). x [n_tokens][hidden], out [n_tokens*top_k][hidden], both of
+ * `dtype` (bf16, fp16, fp32); pos int32 [n_tokens][top_k] with distinct places, as dpa_sort_pairs
+ * writes them. Places outside [0, n_tokens*top_k) are skipped; rows of out that no pair takes are
+ * left as they were. Any hidden >= 1; top_k <= 32; n_tokens*top_k <= 2^30 (all row calls).
+ * Gradient: dpa_unpermute_rows without weights. */
+dpa_status dpa_permute_rows(int dtype, const void* x, const int32_t* pos, int n_tokens, int top_k, int hidden,
+                            void* out, void* stream);
+
+/* y[t] = residual[t] + sum_k weights[t][k] * z[pos[t][k]] (device), added in slot order in fp32
+ * and rounded once. z [n_tokens*top_k][hidden] of `dtype`; weights [n_tokens][top_k] of
+ * weight_dtype (fp32 or fp64; rounded to fp32) or NULL (all 1); residual [n_tokens][hidden] of
+ * out_dtype or NULL, may be y itself; y [n_tokens][hidden] of out_dtype. The two types are equal,
+ * or one of them is fp32. Pairs with a place outside [0, n_tokens*top_k) add nothing (their row
+ * of z is not read): a token without pairs gets its residual, or 0. */
+dpa_status dpa_unpermute_rows(int dtype, const void* z, const int32_t* pos, const void* weights, int weight_dtype,
+                              const void* residual, int out_dtype, int n_tokens, int top_k, int hidden, void* y,
+                              void* stream);
+
+/* Gradients of dpa_unpermute_rows (device): dz[pos[t][k]] = weights[t][k] * dy[t] and
+ * dweights[t][k] = <dy[t], z[pos[t][k]]> (fp32, 0 for pairs without a place). dy, z, dz of `dtype`;
+ * pos with distinct places. Rows of dz that no pair takes are left as they were. The gradient of
+ * the residual is dy. */
+dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z, const int32_t* pos,
+                                       const void* weights, int weight_dtype, int n_tokens, int top_k, int hidden,
+                                       void* dz, float* dweights, void* stream);
+
+/* Matrix product with a fused epilogue (device):
+ *     out = act(x W^T + bias) [* (x U^T + bias_mul)] [+ residual]
+ * x [rows][in_features], w (and w_mul, U) [out_features][in_features], bias and bias_mul
+ * [out_features], all of `dtype` (bf16 or fp16); out and residual [rows][out_features] of
+ * out_dtype (`dtype` or fp32); residual may be out itself. bias, w_mul, bias_mul, residual may be
+ * NULL. Products are summed in fp32; out is rounded once. gelu is v*Phi(v), gelu_tanh its tanh
+ * form. in_features must be a multiple of 8; any rows and out_features >= 1.
+ * ws: device, zero-filled once, at least DPA_LINEAR_WORKSPACE_BYTES (any workspace of this
+ * library serves); it receives the device error flag only. */
+#define DPA_LINEAR_WORKSPACE_BYTES 256
+typedef struct dpa_linear_desc {
+    int32_t rows, in_features, out_features;
+    int32_t dtype, out_dtype, act;
+} dpa_linear_desc;
+dpa_status dpa_linear(const dpa_linear_desc* desc, const void* x, const void* w, const void* bias, const void* w_mul,
+                      const void* bias_mul, const void* residual, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* The same product of each group's rows with that group's weights (device): rows
+ * offsets[e] .. offsets[e+1] - 1 of x, residual and out belong to group e. offsets: int32
+ * [n_groups + 1] on the device, ascending, as dpa_sort_pairs writes them (values outside [0, rows]
+ * read as the nearest row). w, w_mul [n_groups][out_features][in_features]; bias, bias_mul
+ * [n_groups][out_features]. Rows behind the last group are neither used nor written; a group may
+ * be empty. n_groups <= 1024. */
+dpa_status dpa_grouped_linear(const dpa_linear_desc* desc, int n_groups, const void* x, const int32_t* offsets,
+                              const void* w, const void* bias, const void* w_mul, const void* bias_mul,
+                              const void* residual, void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read the device error flag in ws, clear it, and return it
  * (DPA_OK if no device error was recorded). */
 dpa_status dpa_device_status(void* ws, void* stream);

@@ -1,0 +1,113 @@
+"""Argument checks of the expert row sort and the dense products: nothing is launched. CPU only."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from dynamic_any_precision_b200 import dpa  # noqa: E402
+
+BUF = ctypes.c_void_p(16 * 1024)     # never dereferenced: validation fails first
+ODD = ctypes.c_void_p(16 * 1024 + 8)
+WS = 1 << 30
+
+
+def test_sort_workspace_size():
+    f = dpa.lib().dpa_sort_workspace_size
+    assert f(0, 8) == 0 and f(8, 0) == 0 and f(8, 1025) == 0 and f((1 << 30) + 1, 8) == 0
+    assert f(8, 128) == 256
+    sizes = [f(n, 128) for n in (1, 4096, 4097, 65536, 131072, 131073, 1 << 20, 1 << 30)]
+    assert sizes == sorted(sizes)      # a workspace serves every shorter batch
+    with pytest.raises(dpa.DpaError):
+        dpa.sort_workspace_size(0, 8)
+
+
+def test_sort_pairs_arguments():
+    f = dpa.lib().dpa_sort_pairs
+    assert f(BUF, 0, 8, BUF, BUF, BUF, BUF, WS, None) == 1
+    assert f(BUF, 8, 0, BUF, BUF, BUF, BUF, WS, None) == 1
+    assert f(BUF, 8, 1025, BUF, BUF, BUF, BUF, WS, None) == 2
+    assert f(BUF, (1 << 30) + 1, 8, BUF, BUF, BUF, BUF, WS, None) == 2
+    assert f(BUF, 100000, 8, BUF, BUF, BUF, BUF, 256, None) == 3
+    for i in (0, 3, 4, 5, 6):
+        for bad in (None, ODD):
+            args = [BUF, 8, 8, BUF, BUF, BUF, BUF, WS, None]
+            args[i] = bad
+            assert f(*args) == 1, (i, bad)
+
+
+def test_row_call_arguments():
+    L = dpa.lib()
+
+    def permute(dtype=0, x=BUF, pos=BUF, T=4, K=2, H=64, out=BUF):
+        return L.dpa_permute_rows(dtype, x, pos, T, K, H, out, None)
+
+    def unpermute(dtype=0, z=BUF, pos=BUF, w=BUF, wt=2, res=None, odt=0, T=4, K=2, H=64, y=BUF):
+        return L.dpa_unpermute_rows(dtype, z, pos, w, wt, res, odt, T, K, H, y, None)
+
+    def backward(dtype=0, dy=BUF, z=BUF, pos=BUF, w=BUF, wt=2, T=4, K=2, H=64, dz=BUF, dw=BUF):
+        return L.dpa_unpermute_rows_backward(dtype, dy, z, pos, w, wt, T, K, H, dz, dw, None)
+
+    for f in (permute, unpermute, backward):
+        for bad in (dict(T=0), dict(K=0), dict(H=0), dict(T=-1), dict(dtype=3), dict(dtype=-1), dict(pos=None),
+                    dict(pos=ODD)):
+            assert f(**bad) == 1, bad
+        assert f(K=33) == 2
+        assert f(T=1 << 28, K=8) == 2
+    assert permute(x=None) == 1 and permute(x=ODD) == 1 and permute(out=None) == 1 and permute(out=ODD) == 1
+    for bad in (dict(z=None), dict(y=None), dict(z=ODD), dict(y=ODD), dict(res=ODD), dict(w=ODD), dict(wt=0),
+                dict(wt=1), dict(odt=1), dict(odt=3), dict(dtype=1, odt=0)):
+        assert unpermute(**bad) == 1, bad
+    for bad in (dict(dy=None), dict(z=None), dict(w=None), dict(dz=None), dict(dw=None), dict(dy=ODD), dict(dw=ODD),
+                dict(wt=1)):
+        assert backward(**bad) == 1, bad
+
+
+def linear(desc=(4, 64, 32, 0, 0, 0), x=BUF, w=BUF, b=None, u=None, c=None, r=None, out=BUF, ws=BUF, n=256, groups=None,
+           offsets=BUF):
+    d = dpa.LinearDesc(*desc)
+    if groups is None:
+        return dpa.lib().dpa_linear(ctypes.byref(d), x, w, b, u, c, r, out, ws, n, None)
+    return dpa.lib().dpa_grouped_linear(ctypes.byref(d), groups, x, offsets, w, b, u, c, r, out, ws, n, None)
+
+
+@pytest.mark.parametrize("groups", [None, 4])
+def test_product_arguments(groups):
+    def f(**kw):
+        return linear(groups=groups, **kw)
+
+    for desc, code in (((0, 64, 32, 0, 0, 0), 1), ((4, 0, 32, 0, 0, 0), 1), ((4, 64, 0, 0, 0, 0), 1),
+                       ((4, 60, 32, 0, 0, 0), 2), ((4, 64, 32, 2, 2, 0), 1), ((4, 64, 32, 0, 1, 0), 1),
+                       ((4, 64, 32, 1, 0, 0), 1), ((4, 64, 32, 0, 3, 0), 1), ((4, 64, 32, 0, 0, 5), 1),
+                       ((4, 64, 32, 0, 0, -1), 1)):
+        assert f(desc=desc) == code, desc
+    for name in ("x", "w", "out", "ws"):
+        assert f(**{name: None}) == 1 and f(**{name: ODD}) == 1, name
+    for name in ("b", "u", "r"):
+        assert f(**{name: ODD}) == 1, name
+    assert f(u=BUF, c=ODD) == 1
+    assert f(c=BUF) == 1               # a second bias without a second product
+    assert f(n=255) == 3
+    if groups:
+        assert linear(groups=0) == 1 and linear(groups=-1) == 1 and linear(groups=1025) == 2
+        assert f(offsets=None) == 1 and f(offsets=ODD) == 1
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    x, w = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((8, 64), dtype=torch.bfloat16)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    pos = torch.zeros((4, 2), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        dpa.linear(x, w, ws)
+    with pytest.raises(ValueError):
+        dpa.sort_pairs(pos, 8, ws)
+    with pytest.raises(ValueError):
+        dpa.permute_rows(x, pos)
+    with pytest.raises(ValueError):
+        dpa.unpermute_rows(torch.zeros((8, 64)), pos)
+    with pytest.raises(ValueError):
+        dpa.unpermute_rows(torch.zeros((9, 64)), pos)
+    with pytest.raises(ValueError):
+        dpa.linear(x, torch.zeros((8, 32), dtype=torch.bfloat16), ws)
+    with pytest.raises(ValueError):
+        dpa.grouped_linear(x, torch.zeros(3, dtype=torch.int32), torch.zeros((3, 8, 64), dtype=torch.bfloat16), ws)
