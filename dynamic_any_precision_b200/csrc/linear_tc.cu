@@ -7,9 +7,8 @@
 //
 // Orientation: the MMA's M = weight rows (128 per CTA), N = the tile's tokens, so an output
 // feature is a TMEM lane: its bias is a per-thread constant, few tokens cost few MMA columns, and
-// a warp's stores of one token are 32 consecutive features. With a gate (U given) a CTA holds 64
-// features: each 32-lane quadrant has 16 rows of W and the same 16 rows of U, so that the product
-// of both pairs lane t with lane t ^ 16 of one warp.
+// the outputs of a token are turned in shared memory into one run of features. With a gate (U given)
+// a CTA holds 64 features: 64 rows of W and the same 64 rows of U, which meet in that turn.
 //
 // Variants:
 //   CG = 2  two CTAs share one tile (256 weight rows x up to 256 tokens, cta_group::2): each loads
@@ -43,6 +42,7 @@ constexpr int kThreads = (kEpiWarps + 2) * 32;   // 320
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512, kAccCols = 256;
 constexpr int kSmemMax = 232448;
+constexpr int kOutBytes = 2 * 32 * kRowsA * 4;   // epilogue staging, one 32-token chunk per half
 // full[stages], empty[stages], acc_full[2], acc_empty[2], done; then the TMEM address and abort flag
 constexpr int kBarBytes = (2 * kMaxStages + 5) * 8 + 16;
 
@@ -87,14 +87,33 @@ __device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref
 }
 
 // ---- epilogue arithmetic (fp32) ----
-// gelu: v Phi(v) = v erfc(-v / sqrt 2) / 2, without cancellation for negative v. gelu_tanh:
-// v (1 + tanh p) / 2 = v / (1 + exp(-2p)), p = sqrt(2/pi) (v + 0.044715 v^3).
+// The activations use the hardware exponential and reciprocal: a few units in the last place of
+// fp32, of the size of the product's own summation error.
+//   silu       v / (1 + exp(-v))
+//   gelu_tanh  v (1 + tanh p) / 2 = v / (1 + exp(-2p)), p = sqrt(2/pi) (v + 0.044715 v^3)
+//   gelu       v Phi(v). The tail is Phi(-a) = exp(-a^2/2) R(a), a = |v|, which keeps its relative
+//              accuracy for negative v; R is a polynomial of degree 7 in t = 1 / (1 + 0.35 a),
+//              fitted here to exp(a^2/2) Phi(-a) on [0, 14] for the least relative error (3.1e-7;
+//              beyond 14 the exponential is 0 in fp32).
+__device__ __forceinline__ float act_gelu(float v) {
+    const float t = __fdividef(1.f, fmaf(0.35f, fabsf(v), 1.f));
+    float r = fmaf(0.04894237592816353f, t, -0.20211902260780334f);
+    r = fmaf(r, t, 0.24064041674137115f);
+    r = fmaf(r, t, -0.017023101449012756f);
+    r = fmaf(r, t, 0.15596133470535278f);
+    r = fmaf(r, t, 0.13335514068603516f);
+    r = fmaf(r, t, 0.14027033746242523f);
+    r = fmaf(r, t, -2.7315189072396606e-05f);
+    const float q = __expf(-0.5f * v * v) * r;   // Phi(-|v|)
+    return v * (v > 0.f ? 1.f - q : q);
+}
 __device__ __forceinline__ float act_one(float v, int act) {
     switch (act) {
         case DPA_ACT_RELU: return v < 0.f ? 0.f : v;   // NaN stays NaN
-        case DPA_ACT_GELU: return 0.5f * v * erfcf(v * -0.70710678118654752f);
-        case DPA_ACT_GELU_TANH: return v / (1.f + expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-        case DPA_ACT_SILU: return v / (1.f + expf(-v));
+        case DPA_ACT_GELU: return act_gelu(v);
+        case DPA_ACT_GELU_TANH:
+            return __fdividef(v, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * v * v, v, v)));
+        case DPA_ACT_SILU: return __fdividef(v, 1.f + __expf(-v));
         default: return v;
     }
 }
@@ -138,37 +157,98 @@ __device__ __forceinline__ float bias_at(const void* b, int64_t i) {
     return b ? up16<F16>(__ldg(static_cast<const uint16_t*>(b) + i)) : 0.f;
 }
 
-// Adds the residual (all loads first: out may be the residual itself) and stores CNT values of one
-// feature, tokens `step` apart, the first n of them.
-template <bool F16, int CNT>
-__device__ __forceinline__ void store_column(const LinearArgs& a, float (&v)[CNT], int64_t at, int64_t stride, int n) {
+// Eight consecutive outputs of one token. `vec`: rows of whole 8-feature groups (N % 8 == 0, so that
+// every group is 16-byte aligned and wholly inside or outside N); otherwise `cnt` single elements.
+struct Out8 {
+    uint4 lo, hi;   // 16-bit outputs: lo only; fp32: lo, hi
+};
+__device__ __forceinline__ Out8 load_residual(const LinearArgs& a, int64_t at, bool vec, int cnt) {
+    Out8 r;
     if (a.out32) {
-        const float* res = static_cast<const float*>(a.residual);
-        if (res) {
-            float r[CNT];
+        const float* p = static_cast<const float*>(a.residual) + at;
+        if (vec) {
+            r.lo = *reinterpret_cast<const uint4*>(p);
+            r.hi = *reinterpret_cast<const uint4*>(p + 4);
+        } else {
+            uint32_t v[8];
 #pragma unroll
-            for (int j = 0; j < CNT; ++j) r[j] = j < n ? res[at + j * stride] : 0.f;
-#pragma unroll
-            for (int j = 0; j < CNT; ++j) v[j] += r[j];
+            for (int i = 0; i < 8; ++i) v[i] = i < cnt ? __float_as_uint(p[i]) : 0u;
+            r.lo = make_uint4(v[0], v[1], v[2], v[3]);
+            r.hi = make_uint4(v[4], v[5], v[6], v[7]);
         }
-        float* out = static_cast<float*>(a.out);
-#pragma unroll
-        for (int j = 0; j < CNT; ++j)
-            if (j < n) out[at + j * stride] = v[j];
     } else {
-        const uint16_t* res = static_cast<const uint16_t*>(a.residual);
-        if (res) {
-            uint16_t r[CNT];
+        const uint16_t* p = static_cast<const uint16_t*>(a.residual) + at;
+        if (vec) {
+            r.lo = *reinterpret_cast<const uint4*>(p);
+        } else {
+            uint32_t v[4];
 #pragma unroll
-            for (int j = 0; j < CNT; ++j) r[j] = j < n ? res[at + j * stride] : static_cast<uint16_t>(0);
-#pragma unroll
-            for (int j = 0; j < CNT; ++j) v[j] += up16<F16>(r[j]);
+            for (int i = 0; i < 4; ++i)
+                v[i] = (2 * i < cnt ? p[2 * i] : 0u) | (2 * i + 1 < cnt ? static_cast<uint32_t>(p[2 * i + 1]) << 16 : 0u);
+            r.lo = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        uint16_t* out = static_cast<uint16_t*>(a.out);
-#pragma unroll
-        for (int j = 0; j < CNT; ++j)
-            if (j < n) out[at + j * stride] = down16<F16>(v[j]);
     }
+    return r;
+}
+template <bool F16>
+__device__ __forceinline__ void add_residual(const LinearArgs& a, const Out8& r, float (&v)[8]) {
+    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+    if (a.out32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] += up16<F16>(static_cast<uint16_t>(w[i]));
+            v[2 * i + 1] += up16<F16>(static_cast<uint16_t>(w[i] >> 16));
+        }
+    }
+}
+template <bool F16>
+__device__ __forceinline__ void store_out(const LinearArgs& a, const float (&v)[8], int64_t at, bool vec, int cnt) {
+    if (a.out32) {
+        float* p = static_cast<float*>(a.out) + at;
+        if (vec) {   // one 32-byte store
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+                         "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                         : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < cnt) p[i] = v[i];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(a.out) + at;
+        if (vec) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = static_cast<uint32_t>(down16<F16>(v[2 * i])) |
+                       static_cast<uint32_t>(down16<F16>(v[2 * i + 1])) << 16;
+            *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < cnt) p[i] = down16<F16>(v[i]);
+        }
+    }
+}
+
+// Barrier of the four warps of an epilogue half; `ok` comes back false if any of them brought false.
+__device__ __forceinline__ bool half_agree(int half, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(ok)), "r"(1 + half)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void half_sync(int half) {
+    asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + half) : "memory");
 }
 
 // ---- pair (cta_group::2) forms of the tensor-core operations ----
@@ -253,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     const int stages = a.stages, btile = (a.TN / CG) * 128;
     unsigned char* sA = sm;
     unsigned char* sB = sm + stages * kATile;
-    unsigned char* tail = sB + stages * btile;
+    float* s_out = reinterpret_cast<float*>(sB + stages * btile);   // [2][32 tokens][128] epilogue staging
+    unsigned char* tail = sB + stages * btile + kOutBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(tail);
     uint64_t* empty = full + kMaxStages;
     uint64_t* acc_full = empty + kMaxStages;
@@ -355,11 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                     if (CG == 2) bar = mapa_shared(bar, 0);
                     unsigned char* da = sA + s * kATile;
                     if constexpr (GATED) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            load3d<CG>(da + q * 4096, &wmap, kc * kStepK, f0 + q * 16, t.e, bar);
-                            load3d<CG>(da + q * 4096 + 2048, &umap, kc * kStepK, f0 + q * 16, t.e, bar);
-                        }
+                        load3d<CG>(da, &wmap, kc * kStepK, f0, t.e, bar);
+                        load3d<CG>(da + kATile / 2, &umap, kc * kStepK, f0, t.e, bar);
                     } else {
                         load3d<CG>(da, &wmap, kc * kStepK, f0, t.e, bar);
                     }
@@ -426,26 +504,60 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         }
     } else {
         // ================= epilogue =================
+        // The four warps of a half take every second 32-token chunk. A chunk is read from TMEM
+        // (lane = weight row) and turned through shared memory, so that each thread then finishes 8
+        // consecutive features of a token and a token's features leave as one contiguous run. The
+        // staging columns are permuted (kept in place within a 16-byte piece) so that both sides
+        // are free of bank conflicts.
         const int q = warp & 3, half = warp >> 2, R = 32 * q + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+        float* stage = s_out + half * (32 * kRowsA);
+        float* put = stage + (R ^ ((q & 1) * 4 + (q >> 1) * 16));
+        // this thread's features and tokens of a chunk
+        constexpr int kGroups = kFeat / 8, kItems = 32 * kGroups / 128, kTokStep = 32 / kItems;
+        const int ht = R;   // thread of the half
+        const int fg = ht % kGroups, tk0 = ht / kGroups;
+        const int R0 = fg * 8, qr = R0 >> 5;
+        const int sw = (qr & 1) * 4 + (qr >> 1) * 16;
+        const float* get0 = stage + (R0 ^ sw);
+        const float* get1 = stage + ((R0 + 4) ^ sw);
+        const float* gum0 = stage + ((R0 + 64) ^ sw ^ 16);   // the second product (GATED)
+        const float* gum1 = stage + ((R0 + 68) ^ sw ^ 16);
         uint32_t empty_bar[2] = {smem_u32(&acc_empty[0]), smem_u32(&acc_empty[1])};
         if (CG == 2) {
             empty_bar[0] = mapa_shared(empty_bar[0], 0);
             empty_bar[1] = mapa_shared(empty_bar[1], 0);
         }
+        const bool vec = (a.N & 7) == 0;
         int j = 0;
         for (int64_t it = cid; it < ntiles; it += ncl, ++j) {
             const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
             const int b = j & 1;
-            const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + (GATED ? q * 16 + (lane & 15) : R);
-            const bool f_ok = f < a.N;
-            const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
-            const float bias = f_ok ? bias_at<F16>(a.bias, fb) : 0.f;
-            const float bmul = GATED && f_ok ? bias_at<F16>(a.bias_mul, fb) : 0.f;
-            const bool w_ok = mbar_wait_abortable(&acc_full[b], (j >> 1) & 1, s_abort, a.hdr, 0x730);
-            if (!__all_sync(0xffffffffu, w_ok)) break;   // tcgen05.ld below is .sync.aligned
-            tc_fence_after();
+            const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + fg * 8;
+            const int cnt = min(max(a.N - f, 0), 8);
             const int nch = (t.n + 31) >> 5;
+            float bias[8], bmul[8];
+            Out8 res[kItems];
+            if (CG == 2 || S == 1) {   // operands of the epilogue: loaded while the MMAs run
+                const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    bias[i] = i < cnt ? bias_at<F16>(a.bias, fb + i) : 0.f;
+                    bmul[i] = GATED && i < cnt ? bias_at<F16>(a.bias_mul, fb + i) : 0.f;
+                }
+                if (a.residual && cnt > 0) {
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        const int tok = 32 * half + tk0 + i * kTokStep;
+                        if (tok < t.n)
+                            res[i] = load_residual(a, (static_cast<int64_t>(t.row0) + tok) * a.N + f, vec, cnt);
+                    }
+                }
+            }
+            bool w_ok = mbar_wait_abortable(&acc_full[b], (j >> 1) & 1, s_abort, a.hdr, 0x730);
+            w_ok = half_agree(half, w_ok);   // the half leaves together (it synchronises below)
+            if (!w_ok) break;
+            tc_fence_after();
             const uint32_t acc = tmem + lane_base + static_cast<uint32_t>(b) * kAccCols;
             if (CG == 1 && S > 1) {
                 // partial sums [token][128] into the (now idle) stage memory
@@ -472,41 +584,44 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                         else mbarrier_arrive(&acc_empty[b]);
                     }
                 }
-                const int tok0 = 32 * c;
-                if constexpr (GATED) {
-                    // one exchange per token pair: the W lane gets the U value of the even token, the
-                    // U lane the W value of the odd one
-                    const bool wl = (lane & 16) == 0;
-                    float g[16], m[16];
+                if (c > half) half_sync(half);   // the chunk before has been read out
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) {
-                        const float ev = __uint_as_float(v[2 * u]), od = __uint_as_float(v[2 * u + 1]);
-                        const float got = __shfl_xor_sync(0xffffffffu, wl ? od : ev, 16);
-                        g[u] = (wl ? ev : got) + bias;
-                        m[u] = (wl ? got : od) + bmul;
+                for (int u = 0; u < 32; ++u) put[u * kRowsA] = __uint_as_float(v[u]);
+                half_sync(half);
+                if (cnt > 0) {
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        const int in = tk0 + i * kTokStep, tok = 32 * c + in;
+                        if (tok >= t.n) break;
+                        const int64_t at = (static_cast<int64_t>(t.row0) + tok) * a.N + f;
+                        const float4 x0 = *reinterpret_cast<const float4*>(get0 + in * kRowsA);
+                        const float4 x1 = *reinterpret_cast<const float4*>(get1 + in * kRowsA);
+                        float g[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) g[e] += bias[e];
+                        act_many(g, a.act);
+                        if constexpr (GATED) {
+                            const float4 m0 = *reinterpret_cast<const float4*>(gum0 + in * kRowsA);
+                            const float4 m1 = *reinterpret_cast<const float4*>(gum1 + in * kRowsA);
+                            const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) g[e] *= m[e] + bmul[e];
+                        }
+                        if (a.residual) {
+                            add_residual<F16>(a, res[i], g);
+                            if (tok + 64 < t.n) res[i] = load_residual(a, at + 64 * static_cast<int64_t>(a.N), vec, cnt);
+                        }
+                        store_out<F16>(a, g, at, vec, cnt);
                     }
-                    act_many(g, a.act);
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) g[u] *= m[u];
-                    const int first = tok0 + (wl ? 0 : 1);
-                    if (f_ok)
-                        store_column<F16>(a, g, (static_cast<int64_t>(t.row0) + first) * a.N + f,
-                                          2 * static_cast<int64_t>(a.N), (t.n - first + 1) / 2);
-                } else {
-                    float o[32];
-#pragma unroll
-                    for (int u = 0; u < 32; ++u) o[u] = __uint_as_float(v[u]) + bias;
-                    act_many(o, a.act);
-                    if (f_ok)
-                        store_column<F16>(a, o, (static_cast<int64_t>(t.row0) + tok0) * a.N + f, a.N, t.n - tok0);
                 }
             }
-            if (half >= nch) {   // this warp had nothing to read
+            if (half >= nch) {   // this half had nothing to read
                 if (lane == 0) {
                     if (CG == 2) arrive_cluster(empty_bar[b]);
                     else mbarrier_arrive(&acc_empty[b]);
                 }
             }
+            half_sync(half);   // read out before the next tile is staged
         }
     }
     __syncwarp();
@@ -525,12 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                 const int tok = i / kFeat, fi = i - tok * kFeat, f = f0 + fi;
                 if (f >= a.N) continue;
                 const uint32_t off =
-                    static_cast<uint32_t>(tok * kRowsA + (GATED ? (fi >> 4) * 32 + (fi & 15) : fi)) * 4;
+                    static_cast<uint32_t>(tok * kRowsA + fi) * 4;
                 float pv[8], pm[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     pv[r] = r < S ? ld_cluster_f32(peer[r] + off) : 0.f;
-                    pm[r] = GATED && r < S ? ld_cluster_f32(peer[r] + off + 64) : 0.f;
+                    pm[r] = GATED && r < S ? ld_cluster_f32(peer[r] + off + 64 * 4) : 0.f;
                 }
                 float v = pv[0], m = pm[0];
 #pragma unroll
@@ -539,9 +654,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                     m += pm[r];
                 }
                 const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
-                float o[1] = {act_one(v + bias_at<F16>(a.bias, fb), a.act)};
-                if (GATED) o[0] *= m + bias_at<F16>(a.bias_mul, fb);
-                store_column<F16>(a, o, (static_cast<int64_t>(t.row0) + tok) * a.N + f, 0, 1);
+                float o = act_one(v + bias_at<F16>(a.bias, fb), a.act);
+                if (GATED) o *= m + bias_at<F16>(a.bias_mul, fb);
+                const int64_t at = (static_cast<int64_t>(t.row0) + tok) * a.N + f;
+                if (a.out32) {
+                    if (a.residual) o += static_cast<const float*>(a.residual)[at];
+                    static_cast<float*>(a.out)[at] = o;
+                } else {
+                    if (a.residual) o += up16<F16>(static_cast<const uint16_t*>(a.residual)[at]);
+                    static_cast<uint16_t*>(a.out)[at] = down16<F16>(o);
+                }
             }
         }
         cluster_sync();   // no CTA leaves while another reads its partial sums
@@ -634,13 +756,13 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
             while (a.splits < 8 && a.splits < a.ksteps && tiles * (a.splits + 1) <= sms) ++a.splits;
         clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
     }
-    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + kBarBytes + (a.E + 1) * 4;
+    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + kOutBytes + kBarBytes + (a.E + 1) * 4;
     a.stages = (kSmemMax - fixed) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const size_t smem = static_cast<size_t>(a.stages) * stage + fixed;
     alignas(64) CUtensorMap maps[3];
     const uint64_t E = static_cast<uint64_t>(groups);
-    const uint32_t wbox = gated ? 16 : 128;
+    const uint32_t wbox = static_cast<uint32_t>(feat);
     if (!encode_map(&maps[0], w, f16, a.K, a.N, E, wbox, 3) ||
         !encode_map(&maps[1], gated ? w_mul : w, f16, a.K, a.N, E, wbox, 3) ||
         !encode_map(&maps[2], x, f16, a.K, a.rows, 1, static_cast<uint32_t>(a.xbox), 2))
