@@ -124,7 +124,7 @@ dpa_status dpa_unpermute_rows(int dtype, const void* z, const int32_t* pos, cons
     a.T = n_tokens;
     a.K = top_k;
     a.H = hidden;
-    return launched(dpa::launch_unpermute(a, dtype, out_dtype, static_cast<cudaStream_t>(stream)));
+    return launched(dpa::launch_unpermute(a, dtype, out_dtype, static_cast<cudaStream_t>(stream), sms_current()));
 }
 
 dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z, const int32_t* pos,
@@ -146,7 +146,7 @@ dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z,
     a.T = n_tokens;
     a.K = top_k;
     a.H = hidden;
-    return launched(dpa::launch_unpermute_bwd(a, dtype, static_cast<cudaStream_t>(stream)));
+    return launched(dpa::launch_unpermute_bwd(a, dtype, static_cast<cudaStream_t>(stream), sms_current()));
 }
 
 dpa_status dpa_linear(const dpa_linear_desc* desc, const void* x, const void* w, const void* bias, const void* w_mul,

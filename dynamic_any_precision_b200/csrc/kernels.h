@@ -251,7 +251,7 @@ struct UnpermuteArgs {
     void* y;                  // [T][H]
     int T, K, H;
 };
-cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, cudaStream_t stream);
+cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, cudaStream_t stream, int sms);
 
 struct UnpermuteBwdArgs {
     const void* dy;           // [T][H]
@@ -263,7 +263,7 @@ struct UnpermuteBwdArgs {
     float* dweights;          // [T][K], 0 for unrouted pairs
     int T, K, H;
 };
-cudaError_t launch_unpermute_bwd(const UnpermuteBwdArgs& a, int type, cudaStream_t stream);
+cudaError_t launch_unpermute_bwd(const UnpermuteBwdArgs& a, int type, cudaStream_t stream, int sms);
 
 // Matrix products with a fused epilogue, plain or grouped by expert (linear_tc.cu).
 struct LinearArgs {

@@ -13,6 +13,8 @@
 // Positions outside [0, P) are skipped, whatever their value.
 #include <climits>
 #include <cstdint>
+#include <cstring>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -24,12 +26,29 @@ namespace {
 
 // ---------------------------------------------------------------- sort
 
-constexpr int kSortThreads = 512;
-constexpr int kSortOneBlock = 4096;   // pairs that one CTA sorts alone (one launch)
+constexpr int kSortThreads = 1024;
+constexpr int kSortOneBlock = 2048;   // pairs that one CTA sorts alone (one launch)
+// Beyond that: 64 CTAs' chunks of at least 1024 pairs (131072 pairs: 10.5 us with 2048 each, 11.8 us
+// with 1024), 128 chunks once a warp's keys would not stay in registers.
+constexpr int kSortChunk = 1024;
 
 __device__ __forceinline__ int pair_key(const int32_t* idx, int p, int E) {
     const int e = __ldg(idx + p);
     return static_cast<unsigned>(e) < static_cast<unsigned>(E) ? e : E;
+}
+
+// Lanes of the warp with this lane's key, from one ballot per key bit (`bits` covers 0 .. E; lanes
+// without a pair have key -1, all ones). On 128 experts a round of 32 pairs takes a third of the
+// time of the match instruction, which goes through the distinct keys one by one.
+__device__ __forceinline__ unsigned same_key(int key, int bits) {
+    unsigned same = __ballot_sync(0xffffffffu, key >= 0);
+    if (key < 0) same = ~same;
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (key >> b) & 1;
+        const unsigned with = __ballot_sync(0xffffffffu, set);
+        same &= set ? with : ~with;
+    }
+    return same;
 }
 
 // Pairs per expert of each CTA's chunk: hist[b][key], key = E for unrouted pairs.
@@ -39,6 +58,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
     for (int i = threadIdx.x; i < E1; i += kSortThreads) s_cnt[i] = 0;
     __syncthreads();
     pdl_wait();
+    pdl_trigger();   // the ids are final: sort_place_kernel may start on them
     const int p0 = blockIdx.x * a.chunk, p1 = min(a.P - p0, a.chunk) + p0;
     for (int p = p0 + threadIdx.x; p < p1; p += kSortThreads) atomicAdd(&s_cnt[pair_key(a.idx, p, a.E)], 1);
     __syncthreads();
@@ -47,54 +67,87 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
 }
 
 // Places of one CTA's chunk. Each warp owns a contiguous run of the chunk and counts it by key
-// (lanes of equal key found with match), the counts are scanned over warps, earlier chunks and
-// keys, and a second pass over the run hands out the places in order.
+// (lanes of equal key found by ballots), the counts are scanned over warps, earlier chunks and
+// keys, and every pair's place is its key's start plus its rank in the run. IT > 0: the run has at
+// most IT rounds of 32 pairs, whose keys (all loaded at once) and ranks stay in registers; IT = 0:
+// any length, read and ranked a second time.
+// With several chunks the kernel starts beside sort_count_kernel (which lets it go once the ids are
+// final) and waits for it only before it reads the other chunks' counts.
+template <int IT>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
     extern __shared__ int32_t smem[];
     const int E1 = a.E + 1, nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int32_t* s_warp = smem;               // [nw][E1] counts, later the next place
-    int32_t* s_tot = smem + nw * E1;      // [E1] pairs of the key in all chunks
+    int32_t* s_warp = smem;               // [nw][E1] counts, later the first place
+    int32_t* s_tot = smem + nw * E1;      // [E1] pairs of the key in all chunks, later the key's start
     int32_t* s_pre = s_tot + E1;          // [E1] pairs of the key in earlier chunks
     __shared__ int32_t s_sum[32];
-    for (int i = threadIdx.x; i < nw * E1; i += blockDim.x) s_warp[i] = 0;
-    __syncthreads();
-    pdl_wait();
+    for (int i = threadIdx.x; i < (nw + 2) * E1; i += blockDim.x) smem[i] = 0;
+    const bool alone = gridDim.x == 1;
+    if (alone) pdl_wait();
     const int p0 = blockIdx.x * a.chunk, n = min(a.P - p0, a.chunk);
     const int run = (((n + nw - 1) / nw) + 31) & ~31;
     const int w0 = p0 + min(warp * run, n), w1 = p0 + min(warp * run + run, n);
     int32_t* mine = s_warp + warp * E1;
-    for (int b = w0; b < w1; b += 32) {
-        const int p = b + lane;
-        const int key = p < w1 ? pair_key(a.idx, p, a.E) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
-        __syncwarp();
+    const unsigned below = (1u << lane) - 1;
+    const int bits = 32 - __clz(a.E);
+    int key[IT > 0 ? IT : 1], rank[IT > 0 ? IT : 1];
+    if constexpr (IT > 0) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int p = w0 + 32 * i + lane;
+            key[i] = p < w1 ? pair_key(a.idx, p, a.E) : -1;
+        }
     }
-    if (gridDim.x > 1) {
-        for (int e = threadIdx.x; e < E1; e += blockDim.x) {
-            const int32_t* h = a.hist + e;
-            int tot = 0, pre = 0;
-#pragma unroll 8
-            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-                const int c = __ldcg(h + static_cast<size_t>(b) * E1);
-                pre = b == static_cast<int>(blockIdx.x) ? tot : pre;
-                tot += c;
+    __syncthreads();
+    if constexpr (IT > 0) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            if (w0 + 32 * i < w1) {   // warp-uniform
+                const unsigned same = same_key(key[i], bits);
+                const int before = key[i] >= 0 ? mine[key[i]] : 0;
+                rank[i] = before + __popc(same & below);
+                __syncwarp();
+                if (key[i] >= 0 && (same & below) == 0) mine[key[i]] = before + __popc(same);
+                __syncwarp();
             }
-            s_tot[e] = tot;
-            s_pre[e] = pre;
+        }
+    } else {
+        for (int b = w0; b < w1; b += 32) {
+            const int p = b + lane;
+            if (p < w1) atomicAdd(&mine[pair_key(a.idx, p, a.E)], 1);
+        }
+    }
+    if (!alone) {
+        pdl_wait();   // the counts of every chunk
+        // the chunks are split over groups of threads that cover the keys once
+        const int cover = (E1 + 31) & ~31, nb = static_cast<int>(gridDim.x);
+        const int parts = max(1, min(static_cast<int>(blockDim.x) / cover, nb));
+        for (int i = threadIdx.x; i < cover * parts; i += blockDim.x) {
+            const int part = i / cover, e = i - part * cover;
+            if (e >= E1) continue;
+            const int b1 = nb * (part + 1) / parts;
+            int tot = 0, pre = 0;
+#pragma unroll 16
+            for (int b = nb * part / parts; b < b1; ++b) {
+                const int c = __ldcg(a.hist + static_cast<size_t>(b) * E1 + e);
+                tot += c;
+                pre += b < static_cast<int>(blockIdx.x) ? c : 0;
+            }
+            atomicAdd(&s_tot[e], tot);   // whole numbers: the order does not matter
+            atomicAdd(&s_pre[e], pre);
         }
     }
     __syncthreads();
     // counts -> places before this warp's run, per key
     for (int e = threadIdx.x; e < E1; e += blockDim.x) {
-        int acc = gridDim.x > 1 ? s_pre[e] : 0;
-#pragma unroll 4
+        int acc = alone ? 0 : s_pre[e];
+#pragma unroll 8
         for (int w = 0; w < nw; ++w) {
             const int c = s_warp[w * E1 + e];
             s_warp[w * E1 + e] = acc;
             acc += c;
         }
-        if (gridDim.x == 1) s_tot[e] = acc;
+        if (alone) s_tot[e] = acc;
     }
     __syncthreads();
     // exclusive scan of the totals over the keys, `items` consecutive keys per thread
@@ -119,18 +172,30 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
         }
     }
     __syncthreads();
-    for (int b = w0; b < w1; b += 32) {
-        const int p = b + lane;
-        const int key = p < w1 ? pair_key(a.idx, p, a.E) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        if (key >= 0) {
-            const int at = mine[key] + s_tot[key] + __popc(same & ((1u << lane) - 1));
-            a.pos[p] = key < a.E ? at : -1;
-            a.order[at] = p;
+    if constexpr (IT > 0) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            if (key[i] >= 0) {
+                const int p = w0 + 32 * i + lane, at = mine[key[i]] + s_tot[key[i]] + rank[i];
+                a.pos[p] = key[i] < a.E ? at : -1;
+                a.order[at] = p;
+            }
         }
-        __syncwarp();
-        if (key >= 0 && lane == __ffs(same) - 1) mine[key] += __popc(same);
-        __syncwarp();
+    } else {
+        for (int b = w0; b < w1; b += 32) {
+            const int p = b + lane;
+            const int k = p < w1 ? pair_key(a.idx, p, a.E) : -1;
+            const unsigned same = same_key(k, bits);
+            const int before = k >= 0 ? mine[k] : 0;
+            if (k >= 0) {
+                const int at = before + s_tot[k] + __popc(same & below);
+                a.pos[p] = k < a.E ? at : -1;
+                a.order[at] = p;
+            }
+            __syncwarp();
+            if (k >= 0 && (same & below) == 0) mine[k] = before + __popc(same);
+            __syncwarp();
+        }
     }
 }
 
@@ -157,11 +222,85 @@ struct alignas(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Pack {
     T v[VEC];
 };
 
-__device__ __forceinline__ float load_weight(const void* w, int wtype, int64_t i) {
-    if (wtype == DPA_DTYPE_FP64) return static_cast<float>(__ldg(static_cast<const double*>(w) + i));
-    if (wtype == DPA_DTYPE_FP32) return __ldg(static_cast<const float*>(w) + i);
-    return 1.f;   // no weights
+// Slots of one token, held one per lane (top_k <= 32): lane k has the place of slot k (UINT_MAX:
+// unrouted or outside the rows) and its weight (0 then, whatever the weights hold there). Read
+// once per warp, handed out by shuffles.
+struct Slots {
+    unsigned p;
+    float w;
+};
+__device__ __forceinline__ Slots load_slots(const int32_t* pos, const void* weights, int wtype, int64_t t, int K,
+                                            unsigned P, int lane) {
+    Slots s{UINT_MAX, 0.f};
+    if (lane < K) {
+        const unsigned p = static_cast<unsigned>(__ldg(pos + t * K + lane));
+        float w = 1.f;   // no weights
+        if (wtype == DPA_DTYPE_FP64) w = static_cast<float>(__ldg(static_cast<const double*>(weights) + t * K + lane));
+        if (wtype == DPA_DTYPE_FP32) w = __ldg(static_cast<const float*>(weights) + t * K + lane);
+        if (p < P) {
+            s.p = p;
+            s.w = w;
+        }
+    }
+    return s;
 }
+
+// A pack if `on`, else zeros. Written as predicated loads so that the loads of several rows stay
+// together in front of the arithmetic (as branches they were moved to their uses, one at a time:
+// 136 instead of 23 us for 4096 tokens of 8 rows of 2048 bf16).
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_if(const T* p, bool on) {
+    constexpr int kBytes = sizeof(T) * VEC;
+    Pack<T, VEC> out;
+    if constexpr (kBytes % 16 == 0) {
+        uint4 r[kBytes / 16];
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.u32 p, %5, 0;\n\t"
+                "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                : "=&r"(r[i].x), "=&r"(r[i].y), "=&r"(r[i].z), "=&r"(r[i].w)
+                : "l"(reinterpret_cast<const char*>(p) + 16 * i), "r"(static_cast<uint32_t>(on)));
+        memcpy(&out, r, kBytes);
+    } else if constexpr (kBytes == 8) {
+        uint2 r;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %3, 0;\n\t"
+            "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+            "@p ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
+            : "=&r"(r.x), "=&r"(r.y)
+            : "l"(p), "r"(static_cast<uint32_t>(on)));
+        memcpy(&out, &r, kBytes);
+    } else if constexpr (kBytes == 4) {
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %2, 0;\n\t"
+            "mov.b32 %0, 0;\n\t"
+            "@p ld.global.b32 %0, [%1];\n\t}"
+            : "=&r"(r)
+            : "l"(p), "r"(static_cast<uint32_t>(on)));
+        memcpy(&out, &r, kBytes);
+    } else {
+        uint16_t r;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %2, 0;\n\t"
+            "mov.b16 %0, 0;\n\t"
+            "@p ld.global.b16 %0, [%1];\n\t}"
+            : "=&h"(r)
+            : "l"(p), "r"(static_cast<uint32_t>(on)));
+        memcpy(&out, &r, kBytes);
+    }
+    return out;
+}
+
+// Pieces that a lane works on together: four with single elements, so that narrow loads keep as
+// many bytes in flight.
+constexpr int pieces(int vec) { return vec == 1 ? 4 : vec == 2 ? 2 : 1; }
 
 // One warp copies 32*U vectors of one token's row to each of its places. The copy moves bytes
 // only: V is the widest vector that the row length allows.
@@ -190,64 +329,248 @@ __global__ void __launch_bounds__(256) permute_kernel(const V* x, const int32_t*
     }
 }
 
-// One thread per (token, VEC elements); the rows of up to 8 slots are in flight together and are
-// added in slot order in fp32. Weights in fp64 are rounded to fp32 first (2^-24 relative, below
-// the fp32 products' own rounding); the result is rounded once.
+// `wpt` warps per token (8 / wpt tokens per CTA), each over every wpt-th run of 32 * U packs. The
+// rows of up to 8 slots are in flight together and are added in slot order in fp32. Weights in
+// fp64 are rounded to fp32 first (2^-24 relative, below the fp32 products' own rounding); the
+// result is rounded once.
 template <typename ZT, typename YT, int VEC>
-__global__ void __launch_bounds__(256) unpermute_kernel(UnpermuteArgs a, int nvec) {
+__global__ void __launch_bounds__(256) unpermute_kernel(UnpermuteArgs a, int wpt) {
+    constexpr int U = pieces(VEC);
     pdl_wait();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t t = i / nvec;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / wpt) + warp / wpt;
     if (t >= a.T) return;
-    const int64_t c = (i - t * nvec) * VEC;
-    const unsigned P = static_cast<unsigned>(a.T) * a.K;
-    float acc[VEC];
+    const Slots s = load_slots(a.pos, a.weights, a.wtype, t, a.K, static_cast<unsigned>(a.T) * a.K, lane);
+    const YT* res = a.residual ? static_cast<const YT*>(a.residual) + t * a.H : nullptr;
+    YT* yr = static_cast<YT*>(a.y) + t * a.H;
+    for (int c0 = (warp % wpt) * (32 * VEC * U); c0 < a.H; c0 += wpt * (32 * VEC * U)) {   // the warp stays together
+        int c[U];
+        bool in[U];
+        Pack<YT, VEC> r[U];
+        float acc[U][VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-    Pack<YT, VEC> r;
-    if (a.residual) r = *reinterpret_cast<const Pack<YT, VEC>*>(static_cast<const YT*>(a.residual) + t * a.H + c);
-    for (int s0 = 0; s0 < a.K; s0 += 8) {
-        Pack<ZT, VEC> z[8];
-        float w[8];
-        bool on[8];
+        for (int i = 0; i < U; ++i) {
+            c[i] = c0 + (32 * i + lane) * VEC;
+            in[i] = c[i] < a.H;
+            r[i] = load_if<YT, VEC>(res + c[i], res && in[i]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            on[u] = false;
-            if (s0 + u < a.K) {
-                const unsigned p = static_cast<unsigned>(__ldg(a.pos + t * a.K + s0 + u));
-                on[u] = p < P;
-                if (on[u]) {
-                    w[u] = load_weight(a.weights, a.wtype, t * a.K + s0 + u);
-                    z[u] = *reinterpret_cast<const Pack<ZT, VEC>*>(static_cast<const ZT*>(a.z) +
-                                                                   static_cast<int64_t>(p) * a.H + c);
+            for (int j = 0; j < VEC; ++j) acc[i][j] = 0.f;
+        }
+        for (int s0 = 0; s0 < a.K; s0 += 8) {
+            Pack<ZT, VEC> z[8][U];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const unsigned p = __shfl_sync(0xffffffffu, s.p, (s0 + u) & 31);
+                const bool on = s0 + u < a.K && p != UINT_MAX;
+                const ZT* zr = static_cast<const ZT*>(a.z) + static_cast<int64_t>(on ? p : 0u) * a.H;
+#pragma unroll
+                for (int i = 0; i < U; ++i) z[u][i] = load_if<ZT, VEC>(zr + c[i], on && in[i]);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (s0 + u < a.K) {   // unrouted: weight 0 on a row of zeros
+                    const float w = __shfl_sync(0xffffffffu, s.w, (s0 + u) & 31);
+#pragma unroll
+                    for (int i = 0; i < U; ++i)
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) acc[i][j] = fmaf(w, up(z[u][i].v[j]), acc[i][j]);
                 }
             }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (on[u]) {
+        for (int i = 0; i < U; ++i) {
+            if (in[i]) {
+                Pack<YT, VEC> y;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) acc[j] = fmaf(w[u], up(z[u].v[j]), acc[j]);
+                for (int j = 0; j < VEC; ++j) y.v[j] = down<YT>(res ? up(r[i].v[j]) + acc[i][j] : acc[i][j]);
+                *reinterpret_cast<Pack<YT, VEC>*>(yr + c[i]) = y;
             }
         }
     }
-    Pack<YT, VEC> y;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) y.v[j] = down<YT>(a.residual ? up(r.v[j]) + acc[j] : acc[j]);
-    *reinterpret_cast<Pack<YT, VEC>*>(static_cast<YT*>(a.y) + t * a.H + c) = y;
 }
 
-// WPT warps per token (8 / WPT tokens per CTA). Each thread holds its part of dy, reads the same
-// part of up to 8 slots' rows, writes their gradients and adds to their dot products; the dot
-// products are then summed over the lanes by shuffles and over the warps in order.
-template <typename T, int VEC, int WPT>
-__global__ void __launch_bounds__(256) unpermute_bwd_kernel(UnpermuteBwdArgs a) {
+// The same sums for large batches: each warp takes a contiguous range of (token, run) items, a run
+// being kStreamPieces times 32 packs, and keeps the next items' rows on their way into shared
+// memory (asynchronous copies into a ring of its own, nothing shared between threads), so that the
+// loads in flight do not depend on registers. An item's rows are its token's routed slots only,
+// kStreamRows at a time.
+constexpr int kStreamThreads = 128, kStreamStages = 3, kStreamRows = 4, kStreamPieces = 2, kStreamCtas = 3;   // CTAs per SM
+constexpr int kStreamPack = kStreamThreads * 16;
+constexpr int kStreamRes = kStreamRows * kStreamPieces * kStreamPack;        // residual packs behind the rows'
+constexpr int kStreamStage = kStreamRes + kStreamPieces * kStreamThreads * 32;
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 32) {
+        copy_async<16>(dst, src);
+        copy_async<16>(dst + 16, static_cast<const char*>(src) + 16);
+    } else if constexpr (BYTES == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    }
+}
+
+// Position in a warp's items: token, run of the row, and which of the token's routed slots.
+struct Cursor {
+    int64_t t;
+    int left;         // items to go, this one included
+    int run, s0, n;   // n routed slots of the token
+    Slots s;          // lane j: place and weight of the j-th routed slot
+
+    __device__ __forceinline__ void token(const UnpermuteArgs& a, int lane) {
+        s = load_slots(a.pos, a.weights, a.wtype, t, a.K, static_cast<unsigned>(a.T) * a.K, lane);
+        unsigned m = __ballot_sync(0xffffffffu, s.p != UINT_MAX);
+        n = __popc(m);
+        if (n < a.K) {   // close the gaps, keeping the order
+            for (int j = 0; j < lane && m; ++j) m &= m - 1;
+            const int from = m ? __ffs(m) - 1 : 31;
+            __syncwarp();
+            s.p = __shfl_sync(0xffffffffu, s.p, from);
+            s.w = __shfl_sync(0xffffffffu, s.w, from);
+        }
+    }
+    __device__ __forceinline__ void advance(const UnpermuteArgs& a, int runs, int lane) {
+        s0 += kStreamRows;
+        if (s0 < n) return;
+        s0 = 0;
+        --left;
+        if (++run < runs) return;
+        run = 0;
+        ++t;
+        if (left > 0) token(a, lane);
+    }
+};
+
+template <typename ZT, typename YT>
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas) unpermute_stream_kernel(UnpermuteArgs a, int runs) {
+    constexpr int VEC = 16 / sizeof(ZT), kRes = VEC * sizeof(YT);
+    extern __shared__ __align__(16) unsigned char ring[];
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t items = static_cast<int64_t>(a.T) * runs, warps = static_cast<int64_t>(gridDim.x) * (kStreamThreads / 32);
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * (kStreamThreads / 32) + (threadIdx.x >> 5);
+    const int64_t i0 = items * me / warps, i1 = items * (me + 1) / warps;   // items <= 2^30 * 2^24
+    if (i0 >= i1) return;
+    const uint32_t base = smem_u32(ring);
+    Cursor in, out;
+    out.t = i0 / runs;
+    out.run = static_cast<int>(i0 - out.t * runs);
+    out.left = static_cast<int>(i1 - i0);
+    out.s0 = 0;
+    out.token(a, lane);
+    in = out;
+    auto issue = [&](int stage) {
+        if (in.left > 0) {
+            const int c = (in.run * kStreamPieces * 32 + lane) * VEC;
+            const uint32_t dst = base + stage * kStreamStage;
+#pragma unroll
+            for (int u = 0; u < kStreamRows; ++u) {
+                if (in.s0 + u < in.n) {
+                    const unsigned p = __shfl_sync(0xffffffffu, in.s.p, (in.s0 + u) & 31);
+                    const ZT* zr = static_cast<const ZT*>(a.z) + static_cast<int64_t>(p) * a.H + c;
+#pragma unroll
+                    for (int i = 0; i < kStreamPieces; ++i)
+                        if (c + i * 32 * VEC < a.H)
+                            copy_async<16>(dst + (u * kStreamPieces + i) * kStreamPack + threadIdx.x * 16, zr + i * 32 * VEC);
+                }
+            }
+            if (a.residual && in.s0 + kStreamRows >= in.n) {
+                const YT* rr = static_cast<const YT*>(a.residual) + in.t * a.H + c;
+#pragma unroll
+                for (int i = 0; i < kStreamPieces; ++i)
+                    if (c + i * 32 * VEC < a.H)
+                        copy_async<kRes>(dst + kStreamRes + (i * kStreamThreads + threadIdx.x) * kRes, rr + i * 32 * VEC);
+            }
+            in.advance(a, runs, lane);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < kStreamStages - 1; ++i) issue(i);
+    float acc[kStreamPieces][VEC];
+#pragma unroll
+    for (int i = 0; i < kStreamPieces; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[i][j] = 0.f;
+    for (int stage = 0; out.left > 0; stage = stage + 1 == kStreamStages ? 0 : stage + 1) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStreamStages - 2) : "memory");
+        issue(stage == 0 ? kStreamStages - 1 : stage - 1);   // the stage used up by the last round
+        const int c = (out.run * kStreamPieces * 32 + lane) * VEC;
+        const unsigned char* src = ring + stage * kStreamStage;
+#pragma unroll
+        for (int u = 0; u < kStreamRows; ++u) {
+            if (out.s0 + u < out.n) {
+                const float w = __shfl_sync(0xffffffffu, out.s.w, (out.s0 + u) & 31);
+#pragma unroll
+                for (int i = 0; i < kStreamPieces; ++i) {   // lanes behind the row work on what the ring holds
+                    const Pack<ZT, VEC> z = *reinterpret_cast<const Pack<ZT, VEC>*>(
+                        src + (u * kStreamPieces + i) * kStreamPack + threadIdx.x * 16);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) acc[i][j] = fmaf(w, up(z.v[j]), acc[i][j]);
+                }
+            }
+        }
+        if (out.s0 + kStreamRows >= out.n) {
+#pragma unroll
+            for (int i = 0; i < kStreamPieces; ++i) {
+                Pack<YT, VEC> y;
+                if (a.residual) {
+                    const Pack<YT, VEC> r = *reinterpret_cast<const Pack<YT, VEC>*>(
+                        src + kStreamRes + (i * kStreamThreads + threadIdx.x) * kRes);
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) acc[i][j] = up(r.v[j]) + acc[i][j];
+                }
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    y.v[j] = down<YT>(acc[i][j]);
+                    acc[i][j] = 0.f;
+                }
+                if (c + i * 32 * VEC < a.H)
+                    *reinterpret_cast<Pack<YT, VEC>*>(static_cast<YT*>(a.y) + out.t * a.H + c + i * 32 * VEC) = y;
+            }
+        }
+        out.advance(a, runs, lane);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Sums of 8 values over the lanes of a warp; lane l returns the sum of value l & 7 (in the order of
+// the butterfly, the same in every run): halves of the values are exchanged while there are several.
+__device__ __forceinline__ float warp_sums8(const float (&v)[8], int lane) {
+    float a[4], b[2], c;
+    const bool h0 = lane & 4, h1 = lane & 2, h2 = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float got = __shfl_xor_sync(0xffffffffu, h0 ? v[i] : v[i + 4], 4);
+        a[i] = (h0 ? v[i + 4] : v[i]) + got;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float got = __shfl_xor_sync(0xffffffffu, h1 ? a[i] : a[i + 2], 2);
+        b[i] = (h1 ? a[i + 2] : a[i]) + got;
+    }
+    {
+        const float got = __shfl_xor_sync(0xffffffffu, h2 ? b[0] : b[1], 1);
+        c = (h2 ? b[1] : b[0]) + got;
+    }
+    c += __shfl_xor_sync(0xffffffffu, c, 8);
+    c += __shfl_xor_sync(0xffffffffu, c, 16);
+    return c;
+}
+
+// `wpt` warps per token (8 / wpt tokens per CTA). Each thread reads its part of dy and the same part
+// of up to 8 slots' rows, writes the rows' gradients and adds to their dot products; the dot
+// products are then summed over the lanes and, in order, over the token's warps.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) unpermute_bwd_kernel(UnpermuteBwdArgs a, int wpt) {
+    constexpr int U = pieces(VEC);
     __shared__ float s_dot[8][8];
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wt = warp % WPT;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / WPT) + warp / WPT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wt = warp % wpt;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / wpt) + warp / wpt;
     const bool live = t < a.T;
-    const unsigned P = static_cast<unsigned>(a.T) * a.K;
+    Slots s{UINT_MAX, 0.f};
+    if (live) s = load_slots(a.pos, a.weights, a.wtype, t, a.K, static_cast<unsigned>(a.T) * a.K, lane);
     const T* dyr = static_cast<const T*>(a.dy) + t * a.H;
     for (int s0 = 0; s0 < a.K; s0 += 8) {
         float dot[8], w[8];
@@ -255,48 +578,68 @@ __global__ void __launch_bounds__(256) unpermute_bwd_kernel(UnpermuteBwdArgs a) 
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             dot[u] = 0.f;
-            p[u] = UINT_MAX;
-            if (live && s0 + u < a.K) {
-                p[u] = static_cast<unsigned>(__ldg(a.pos + t * a.K + s0 + u));
-                if (p[u] < P) w[u] = load_weight(a.weights, a.wtype, t * a.K + s0 + u);
-            }
+            p[u] = __shfl_sync(0xffffffffu, s.p, (s0 + u) & 31);
+            w[u] = __shfl_sync(0xffffffffu, s.w, (s0 + u) & 31);
+            if (s0 + u >= a.K) p[u] = UINT_MAX;
         }
-        for (int c = (wt * 32 + lane) * VEC; live && c < a.H; c += 32 * WPT * VEC) {
-            const Pack<T, VEC> dy = *reinterpret_cast<const Pack<T, VEC>*>(dyr + c);
-            Pack<T, VEC> z[8];
+        for (int c0 = wt * (32 * VEC * U); live && c0 < a.H; c0 += wpt * (32 * VEC * U)) {
+            Pack<T, VEC> dy[U], z[8][U];
+            int c[U];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (p[u] < P)
-                    z[u] = *reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(a.z) +
-                                                                  static_cast<int64_t>(p[u]) * a.H + c);
+            for (int i = 0; i < U; ++i) {
+                c[i] = c0 + (32 * i + lane) * VEC;
+                dy[i] = load_if<T, VEC>(dyr + c[i], c[i] < a.H);
+            }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if (p[u] < P) {
+                const T* zr = static_cast<const T*>(a.z) + static_cast<int64_t>(p[u] != UINT_MAX ? p[u] : 0u) * a.H;
+#pragma unroll
+                for (int i = 0; i < U; ++i) z[u][i] = load_if<T, VEC>(zr + c[i], p[u] != UINT_MAX && c[i] < a.H);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (p[u] == UINT_MAX) continue;
+                T* dzr = static_cast<T*>(a.dz) + static_cast<int64_t>(p[u]) * a.H;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
                     Pack<T, VEC> g;
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
-                        const float d = up(dy.v[j]);
-                        dot[u] = fmaf(d, up(z[u].v[j]), dot[u]);
+                        const float d = up(dy[i].v[j]);
+                        dot[u] = fmaf(d, up(z[u][i].v[j]), dot[u]);
                         g.v[j] = down<T>(w[u] * d);
                     }
-                    *reinterpret_cast<Pack<T, VEC>*>(static_cast<T*>(a.dz) + static_cast<int64_t>(p[u]) * a.H + c) = g;
+                    if (c[i] < a.H) *reinterpret_cast<Pack<T, VEC>*>(dzr + c[i]) = g;
                 }
             }
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            for (int o = 16; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-            if (lane == 0) s_dot[warp][u] = dot[u];
+        __syncwarp();
+        float d = warp_sums8(dot, lane);   // 0 for unrouted slots
+        if (wpt > 1) {
+            if (lane < 8) s_dot[warp][lane] = d;
+            __syncthreads();
+            if (wt == 0 && lane < 8) {
+                d = 0.f;
+                for (int v = 0; v < wpt; ++v) d += s_dot[warp + v][lane];
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        if (live && wt == 0 && lane < 8 && s0 + lane < a.K) {
-            float d = 0.f;
-#pragma unroll
-            for (int v = 0; v < WPT; ++v) d += s_dot[warp + v][lane];
-            a.dweights[t * a.K + s0 + lane] = d;
-        }
-        __syncthreads();
+        if (live && wt == 0 && lane < 8 && s0 + lane < a.K) a.dweights[t * a.K + s0 + lane] = d;
     }
+}
+
+// Warps per token: enough to fill the GPU (32 warps per SM), no more than the row has runs.
+int warps_per_token(int T, int H, int vec, int sms) {
+    int w = 1;
+    while (w < 8 && static_cast<int64_t>(T) * w < 32 * sms && 32 * w * vec * pieces(vec) < H) w *= 2;
+    return w;
+}
+
+// Elements per pack: the widest of 16 bytes (of the narrower type) that divides the row.
+int pack_of(int H, int widest) {
+    int v = widest;
+    while (H % v) v /= 2;
+    return v;
 }
 
 template <typename V>
@@ -314,52 +657,59 @@ cudaError_t permute_vec(const void* x, const int32_t* pos, void* out, int T, int
 }
 
 template <typename ZT, typename YT>
-cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream) {
-    constexpr int VEC = sizeof(ZT) < sizeof(YT) ? 16 / sizeof(YT) * 2 : 16 / sizeof(ZT);
-    const bool vec = a.H % VEC == 0;
-    int nvec = vec ? a.H / VEC : a.H;
-    const int64_t blocks = (static_cast<int64_t>(a.T) * nvec + 255) / 256;
-    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream, int sms) {
+    constexpr int kWidest = sizeof(ZT) == 2 ? 8 : 4;
+    const int vec = pack_of(a.H, kWidest);
+    int wpt = warps_per_token(a.T, a.H, vec, sms);
     UnpermuteArgs b = a;
-    void* args[] = {&b, &nvec};
-    const void* fn = vec ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, VEC>)
-                         : reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, 1>);
-    return launch_pdl_raw(fn, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, args);
-}
-
-template <typename T, int VEC>
-cudaError_t unpermute_bwd_vec(const UnpermuteBwdArgs& a, cudaStream_t stream) {
-    const int lanes = (a.H + VEC - 1) / VEC;
-    UnpermuteBwdArgs b = a;
-    void* args[] = {&b};
-    auto go = [&](const void* fn, int wpt) {
-        const int per = 8 / wpt;
-        return launch_pdl_raw(fn, dim3((a.T - 1) / per + 1), dim3(256), 0, stream, args);
-    };
-    if (lanes <= 32) return go(reinterpret_cast<const void*>(unpermute_bwd_kernel<T, VEC, 1>), 1);
-    if (lanes <= 64) return go(reinterpret_cast<const void*>(unpermute_bwd_kernel<T, VEC, 2>), 2);
-    if (lanes <= 128) return go(reinterpret_cast<const void*>(unpermute_bwd_kernel<T, VEC, 4>), 4);
-    return go(reinterpret_cast<const void*>(unpermute_bwd_kernel<T, VEC, 8>), 8);
+    constexpr int kRun = kStreamPieces * 32 * kWidest;
+    const int runs = (a.H - 1) / kRun + 1;
+    const int ctas = kStreamCtas * sms;
+    // two items per warp at least (1024 tokens of 8 rows of 2048 bf16: 7.5 us, against 8.9 us for the
+    // kernel without the ring; 4096 tokens: 27 against 40 us)
+    if (vec == kWidest && static_cast<int64_t>(a.T) * runs >= static_cast<int64_t>(ctas) * (kStreamThreads / 32) * 2) {
+        const void* fn = reinterpret_cast<const void*>(unpermute_stream_kernel<ZT, YT>);
+        const size_t smem = static_cast<size_t>(kStreamStages) * kStreamStage;
+        const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+        int r = runs;
+        void* sargs[] = {&b, &r};
+        return launch_pdl_raw(fn, dim3(ctas), dim3(kStreamThreads), smem, stream, sargs);
+    }
+    void* args[] = {&b, &wpt};
+    const void* fn = vec == kWidest ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, kWidest>)
+                     : vec == 4     ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, 4>)
+                     : vec == 2     ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, 2>)
+                                    : reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, 1>);
+    return launch_pdl_raw(fn, dim3((a.T - 1) / (8 / wpt) + 1), dim3(256), 0, stream, args);
 }
 
 template <typename T>
-cudaError_t unpermute_bwd_type(const UnpermuteBwdArgs& a, cudaStream_t stream) {
-    constexpr int VEC = 16 / sizeof(T);
-    return a.H % VEC == 0 ? unpermute_bwd_vec<T, VEC>(a, stream) : unpermute_bwd_vec<T, 1>(a, stream);
+cudaError_t unpermute_bwd_type(const UnpermuteBwdArgs& a, cudaStream_t stream, int sms) {
+    constexpr int kWidest = 16 / sizeof(T);
+    const int vec = pack_of(a.H, kWidest);
+    int wpt = warps_per_token(a.T, a.H, vec, sms);
+    UnpermuteBwdArgs b = a;
+    void* args[] = {&b, &wpt};
+    const void* fn = vec == kWidest ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, kWidest>)
+                     : vec == 4     ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 4>)
+                     : vec == 2     ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 2>)
+                                    : reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 1>);
+    return launch_pdl_raw(fn, dim3((a.T - 1) / (8 / wpt) + 1), dim3(256), 0, stream, args);
 }
 
 }  // namespace
 
 int sort_chunk_pairs(int P) {
     if (P <= kSortOneBlock) return P;
-    const int per = (P - 1) / 128 + 1;   // at most 128 chunks
-    return per <= 1024 ? 1024 : (per + 511) & ~511;
+    const int per = (P - 1) / 64 + 1 <= 8 * kSortThreads ? (P - 1) / 64 + 1 : (P - 1) / 128 + 1;
+    return (per + kSortChunk - 1) / kSortChunk * kSortChunk;
 }
 
 // Counts of the chunks of any batch of up to P pairs.
 size_t sort_hist_bytes(int P, int E) {
     if (P <= kSortOneBlock) return 0;
-    const int nb = (P - 1) / 1024 + 1;
+    const int nb = (P - 1) / kSortChunk + 1;
     return static_cast<size_t>(nb < 128 ? nb : 128) * (E + 1) * 4;
 }
 
@@ -378,14 +728,19 @@ cudaError_t launch_sort_pairs(const SortArgs& a, cudaStream_t stream) {
         threads = ((a.P + 31) / 32) * 32;
         threads = threads < 128 ? 128 : threads > kSortThreads ? kSortThreads : threads;
     }
+    const int rounds = (((b.chunk < a.P ? b.chunk : a.P) + threads / 32 - 1) / (threads / 32) + 31) / 32;   // per warp
+    const void* fn = rounds <= 1   ? reinterpret_cast<const void*>(sort_place_kernel<1>)
+                     : rounds <= 4 ? reinterpret_cast<const void*>(sort_place_kernel<4>)
+                     : rounds <= 8 ? reinterpret_cast<const void*>(sort_place_kernel<8>)
+                                   : reinterpret_cast<const void*>(sort_place_kernel<0>);
     const size_t smem = sort_smem_bytes(threads / 32, a.E);
     if (smem > 48 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void*>(sort_place_kernel),
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(sort_smem_bytes(kSortThreads / 32, kSortMaxExperts)));
+        const cudaError_t err =
+            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(sort_smem_bytes(kSortThreads / 32, kSortMaxExperts)));
         if (err != cudaSuccess) return err;
     }
-    return launch_pdl_raw(reinterpret_cast<const void*>(sort_place_kernel), dim3(nb), dim3(threads), smem, stream, args);
+    return launch_pdl_raw(fn, dim3(nb), dim3(threads), smem, stream, args);
 }
 
 cudaError_t launch_permute_pairs(int elem_bytes, const void* x, const int32_t* pos, int T, int K, int H, void* out,
@@ -401,22 +756,22 @@ cudaError_t launch_permute_pairs(int elem_bytes, const void* x, const int32_t* p
     }
 }
 
-cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, cudaStream_t stream) {
-    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_BF16) return unpermute_types<__nv_bfloat16, __nv_bfloat16>(a, stream);
-    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP16) return unpermute_types<__half, __half>(a, stream);
-    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP32) return unpermute_types<float, float>(a, stream);
-    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_FP32) return unpermute_types<__nv_bfloat16, float>(a, stream);
-    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP32) return unpermute_types<__half, float>(a, stream);
-    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_BF16) return unpermute_types<float, __nv_bfloat16>(a, stream);
-    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP16) return unpermute_types<float, __half>(a, stream);
+cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, cudaStream_t stream, int sms) {
+    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_BF16) return unpermute_types<__nv_bfloat16, __nv_bfloat16>(a, stream, sms);
+    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP16) return unpermute_types<__half, __half>(a, stream, sms);
+    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP32) return unpermute_types<float, float>(a, stream, sms);
+    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_FP32) return unpermute_types<__nv_bfloat16, float>(a, stream, sms);
+    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP32) return unpermute_types<__half, float>(a, stream, sms);
+    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_BF16) return unpermute_types<float, __nv_bfloat16>(a, stream, sms);
+    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP16) return unpermute_types<float, __half>(a, stream, sms);
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_unpermute_bwd(const UnpermuteBwdArgs& a, int type, cudaStream_t stream) {
+cudaError_t launch_unpermute_bwd(const UnpermuteBwdArgs& a, int type, cudaStream_t stream, int sms) {
     switch (type) {
-        case DPA_DTYPE_BF16: return unpermute_bwd_type<__nv_bfloat16>(a, stream);
-        case DPA_DTYPE_FP16: return unpermute_bwd_type<__half>(a, stream);
-        case DPA_DTYPE_FP32: return unpermute_bwd_type<float>(a, stream);
+        case DPA_DTYPE_BF16: return unpermute_bwd_type<__nv_bfloat16>(a, stream, sms);
+        case DPA_DTYPE_FP16: return unpermute_bwd_type<__half>(a, stream, sms);
+        case DPA_DTYPE_FP32: return unpermute_bwd_type<float>(a, stream, sms);
         default: return cudaErrorInvalidValue;
     }
 }
