@@ -39,6 +39,7 @@ CU_SOURCES = {
     "rates.cu": ["--fmad=false"],
     "pairs.cu": [],
     "linear_tc.cu": [],
+    "linear_few.cu": [],
     "dense_abi.cu": [],
 }
 CPP_SOURCES = {"encode.cpp": ["-O2", "-ffp-contract=off", "-fno-fast-math"]}

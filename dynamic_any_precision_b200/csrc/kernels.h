@@ -282,5 +282,9 @@ struct LinearArgs {
 };
 cudaError_t launch_linear(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
                           cudaStream_t stream, int sms);
+// The plain product for at most kFewRows rows (linear_few.cu).
+constexpr int kFewRows = 32;
+cudaError_t launch_linear_few(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
+                              cudaStream_t stream);
 
 }  // namespace dpa

@@ -1,0 +1,145 @@
+// The matrix products of dpa_linear for few rows (one token up to a small decode batch): bound by
+// reading the weights once, and at these sizes (8 MB: 1.3 us of memory time) by latency.
+//
+// A CTA computes 16 output features for all rows, its 8 warps taking every 8th block of 32 inputs.
+// Each lane reads 16-byte pieces of two weight rows straight into registers, all of a warp's loads
+// of a round in flight at once, with no shared memory, barrier or TMEM set-up in front of them. The
+// products go through m16n8k16 MMAs with the weight rows as M and the tokens as N; the tensor rate
+// does not matter here. The MMA's order of the 16 inputs is free as long as both operands use the
+// same one, so a lane's 16-byte piece (8 inputs) feeds two MMAs as it is. The warps' partial sums
+// are added in warp order in shared memory (the same in every run), then the epilogue runs.
+#include "common.cuh"
+#include "epilogue.cuh"
+#include "kernels.h"
+
+namespace dpa {
+namespace {
+
+constexpr int kWarps = 8, kFeat = 16, kBlockK = 32;
+
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 load_weights(const uint16_t* p) {   // read once: kept out of L1
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// NT tiles of 8 tokens; MATS weight matrices (2: gated).
+template <bool F16, int MATS, int NT>
+__global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(LinearArgs a, const uint16_t* x, const uint16_t* w,
+                                                               const uint16_t* u) {
+    __shared__ float s_part[kWarps][MATS][8 * NT][kFeat + 1];
+    constexpr int kRound = MATS * NT >= 4 ? 2 : 4;   // blocks whose loads are in flight together
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int f0 = blockIdx.x * kFeat;
+    const int nblk = (a.K + kBlockK - 1) / kBlockK;
+    // rows behind the last feature read the last one, and are not stored
+    const int64_t r0 = static_cast<int64_t>(min(f0 + g, a.N - 1)) * a.K + 8 * c;
+    const int64_t r1 = static_cast<int64_t>(min(f0 + g + 8, a.N - 1)) * a.K + 8 * c;
+    const uint16_t* mat[2] = {w, u};
+    float acc[MATS][NT][4];
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.f;
+    pdl_wait();
+    for (int b = warp; b < nblk; b += kWarps * kRound) {
+        uint4 av[kRound][MATS][2], bv[kRound][NT];
+#pragma unroll
+        for (int i = 0; i < kRound; ++i) {
+            const int k = (b + i * kWarps) * kBlockK;
+            const bool in = k + 8 * c < a.K;   // K % 8 == 0: a piece is wholly inside or outside
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) {
+                av[i][m][0] = in ? load_weights(mat[m] + r0 + k) : make_uint4(0, 0, 0, 0);
+                av[i][m][1] = in ? load_weights(mat[m] + r1 + k) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int tok = 8 * t + g;
+                bv[i][t] = in && tok < a.rows
+                               ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<int64_t>(tok) * a.K + k + 8 * c))
+                               : make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRound; ++i)
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint4 p = av[i][m][0], q = av[i][m][1], s = bv[i][t];
+                    mma16<F16>(acc[m][t], p.x, q.x, p.y, q.y, s.x, s.y);
+                    mma16<F16>(acc[m][t], p.z, q.z, p.w, q.w, s.z, s.w);
+                }
+    }
+#pragma unroll
+    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {   // accumulator i: feature g + 8 (i / 2), token 2c + i % 2
+            s_part[warp][m][8 * t + 2 * c][g] = acc[m][t][0];
+            s_part[warp][m][8 * t + 2 * c + 1][g] = acc[m][t][1];
+            s_part[warp][m][8 * t + 2 * c][g + 8] = acc[m][t][2];
+            s_part[warp][m][8 * t + 2 * c + 1][g + 8] = acc[m][t][3];
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.rows * kFeat; i += kWarps * 32) {
+        const int tok = i / kFeat, fi = i % kFeat, f = f0 + fi;
+        if (f >= a.N) continue;
+        float v[MATS];
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+            v[m] = 0.f;
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) v[m] += s_part[q][m][tok][fi];
+        }
+        float o = act_one(v[0] + bias_at<F16>(a.bias, f), a.act);
+        if (MATS == 2) o *= v[MATS - 1] + bias_at<F16>(a.bias_mul, f);
+        const int64_t at = static_cast<int64_t>(tok) * a.N + f;
+        if (a.out32) {
+            if (a.residual) o += static_cast<const float*>(a.residual)[at];
+            static_cast<float*>(a.out)[at] = o;
+        } else {
+            if (a.residual) o += up16<F16>(static_cast<const uint16_t*>(a.residual)[at]);
+            static_cast<uint16_t*>(a.out)[at] = down16<F16>(o);
+        }
+    }
+}
+
+template <bool F16, int MATS>
+const void* pick(int rows) {
+    if (rows <= 8) return reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 1>);
+    if (rows <= 16) return reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 2>);
+    return reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 4>);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
+                              cudaStream_t stream) {
+    const void* fn = w_mul ? (f16 ? pick<true, 2>(a.rows) : pick<false, 2>(a.rows))
+                           : (f16 ? pick<true, 1>(a.rows) : pick<false, 1>(a.rows));
+    LinearArgs b = a;
+    void* args[] = {&b, &x, &w, &w_mul};
+    return launch_pdl_raw(fn, dim3((a.N - 1) / kFeat + 1), dim3(kWarps * 32), 0, stream, args);
+}
+
+}  // namespace dpa

@@ -366,48 +366,83 @@ def residual_rmsnorm(h, x, y=None, stream=None):
 
 # ------------------------------------------------------------- dense experts: rows and products
 
-def _dtype(t) -> int:
-    """DTYPE_* of a tensor's elements (int16 and uint16 tensors hold bf16 bit patterns)."""
+_DTYPES = None
+_current_device = _raw_stream = None
+
+
+def _torch_tables():
+    """Element types and the current device and stream, looked up once (torch is imported late)."""
+    global _DTYPES, _current_device, _raw_stream
     import torch
-    code = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.uint16: DTYPE_BF16,
-            torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32, torch.float64: DTYPE_FP64}.get(t.dtype)
+    _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.uint16: DTYPE_BF16,
+               torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32, torch.float64: DTYPE_FP64,
+               torch.int32: "int32", torch.uint8: "uint8"}
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _dtype(t):
+    """DTYPE_* of a tensor's elements (int16 and uint16 tensors hold bf16 bit patterns), or "int32"
+    or "uint8"."""
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"unsupported element type {t.dtype}")
     return code
 
 
-def _expect(t, name: str, shape, dtype=None, like=None):
-    """Check a tensor argument: shape, element type (a torch dtype or a DTYPE_* code), device."""
-    if tuple(t.shape) != tuple(shape):
+def _float_type(t) -> int:
+    """_dtype of a tensor that has to hold floating-point rows."""
+    code = _dtype(t)
+    if not isinstance(code, int):
+        raise ValueError(f"unsupported element type {t.dtype}")
+    return code
+
+
+def _arg(t, name: str, shape, code, dev: int) -> int:
+    """Pointer of a tensor argument, after checking its shape, element type (a code of _dtype),
+    device index and layout."""
+    if t.shape == shape and _DTYPES.get(t.dtype) == code and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dtype is not None and (_dtype(t) if isinstance(dtype, int) else t.dtype) != dtype:
+    if _dtype(t) != code:
         raise ValueError(f"{name}: unexpected element type {t.dtype}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name}: expected a tensor on {like.device}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-class _On:
-    """The device of a tensor made current for one call, and the stream of the call on it: the
-    given stream, or that device's current one."""
+def _opt(t, name: str, shape, code, dev: int):
+    return None if t is None else _arg(t, name, shape, code, dev)
 
-    def __init__(self, t, stream):
+
+def _device(t) -> int:
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if _DTYPES is None:
+        _torch_tables()
+    return t.get_device()
+
+
+def _call(fn, where: str, dev: int, stream, *args):
+    """Run a device call on `dev`, on the given stream or that device's current one."""
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if _current_device() == dev:
+        st = fn(*args, raw)
+    else:
         import torch
-        if not t.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        self.device, self.stream = t.device.index, stream
-        self.other = torch.cuda.current_device() != self.device
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != DPA_OK:
+        raise DpaError(st, where)
 
-    def __enter__(self) -> int:
-        import torch
-        if self.other:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        s = torch.cuda.current_stream(self.device) if self.stream is None else self.stream
-        return s.cuda_stream
 
-    def __exit__(self, *exc):
-        if self.other:
-            self.guard.__exit__(*exc)
+def _new(like, shape, dtype, stream):
+    """A new tensor on `like`'s device, taken from the memory of the stream that the call runs on."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def sort_workspace_size(n_pairs: int, n_experts: int) -> int:
@@ -436,22 +471,16 @@ def sort_pairs(idx, n_experts: int, ws, pos=None, order=None, offsets=None, stre
     ids outside [0, n_experts) are not routed). Returns (pos in idx's shape, order [P], offsets
     [n_experts + 1]), int32: the place of each pair (-1 if not routed), the pair at each place
     (unrouted ones last), the places before each expert."""
-    import torch
-    P = idx.numel()
-    _expect(idx, "idx", idx.shape, torch.int32)
-    _expect(ws, "ws", ws.shape, torch.uint8, like=idx)
+    dev, P = _device(idx), idx.numel()
     if pos is None:
-        pos = torch.empty_like(idx)
+        pos = _new(idx, idx.shape, idx.dtype, stream)
     if order is None:
-        order = torch.empty(P, dtype=torch.int32, device=idx.device)
+        order = _new(idx, (P,), idx.dtype, stream)
     if offsets is None:
-        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=idx.device)
-    _expect(pos, "pos", idx.shape, torch.int32, like=idx)
-    _expect(order, "order", (P,), torch.int32, like=idx)
-    _expect(offsets, "offsets", (n_experts + 1,), torch.int32, like=idx)
-    with _On(idx, stream) as s:
-        _check(lib().dpa_sort_pairs(_dptr(idx), P, n_experts, _dptr(pos), _dptr(order), _dptr(offsets), _dptr(ws),
-                                    ws.numel(), s), "dpa_sort_pairs")
+        offsets = _new(idx, (n_experts + 1,), idx.dtype, stream)
+    _call(lib().dpa_sort_pairs, "dpa_sort_pairs", dev, stream, _arg(idx, "idx", idx.shape, "int32", dev), P, n_experts,
+          _arg(pos, "pos", idx.shape, "int32", dev), _arg(order, "order", (P,), "int32", dev),
+          _arg(offsets, "offsets", (n_experts + 1,), "int32", dev), _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
     return pos, order, offsets
 
 
@@ -459,15 +488,12 @@ def permute_rows(x, pos, out=None, stream=None):
     """out[pos[t][k]] = x[t]. x: [T][H] bf16 (or int16 bits), fp16 or fp32; pos: int32 [T][K] from
     sort_pairs. Returns out [T*K][H]; rows that no pair takes are left as they were (with out=None:
     uninitialised)."""
-    import torch
-    T, H = x.shape
-    K = pos.shape[-1]
-    _expect(pos, "pos", (T, K), torch.int32, like=x)
+    dev, code = _device(x), _float_type(x)
+    (T, H), K = x.shape, pos.shape[-1]
     if out is None:
-        out = torch.empty((T * K, H), dtype=x.dtype, device=x.device)
-    _expect(out, "out", (T * K, H), _dtype(x), like=x)
-    with _On(x, stream) as s:
-        _check(lib().dpa_permute_rows(_dtype(x), _dptr(x), _dptr(pos), T, K, H, _dptr(out), s), "dpa_permute_rows")
+        out = _new(x, (T * K, H), x.dtype, stream)
+    _call(lib().dpa_permute_rows, "dpa_permute_rows", dev, stream, code, _arg(x, "x", x.shape, _dtype(x), dev),
+          _arg(pos, "pos", (T, K), "int32", dev), T, K, H, _arg(out, "out", (T * K, H), code, dev))
     return out
 
 
@@ -476,82 +502,72 @@ def permute_rows_backward(dout, pos, dx=None, stream=None):
     return unpermute_rows(dout, pos, None, out=dx, stream=stream)
 
 
+def _out(out, shape, like, residual, out_dtype, stream):
+    """The output tensor of a call: the given one, or a new one of out_dtype (default: the
+    residual's type, else `like`'s)."""
+    if out is None:
+        return _new(like, shape, out_dtype or (like if residual is None else residual).dtype, stream)
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out: unexpected element type {out.dtype}")
+    return out
+
+
 def unpermute_rows(z, pos, weights=None, residual=None, out=None, out_dtype=None, stream=None):
     """y[t] = residual[t] + sum_k weights[t][k] * z[pos[t][k]]. z: [T*K][H]; pos: int32 [T][K];
     weights: fp32 or fp64 [T][K] (None: all 1); residual: [T][H] of y's type, may be `out`. y has
     out_dtype (default: residual's, else z's): z's own type, or one of the two is fp32."""
-    import torch
-    T, K = pos.shape
-    P, H = z.shape
-    _expect(pos, "pos", (T, K), torch.int32, like=z)
-    _expect(z, "z", (T * K, H))
-    if out is None:
-        dt = out_dtype or (z.dtype if residual is None else residual.dtype)
-        out = torch.empty((T, H), dtype=dt, device=z.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out: unexpected element type {out.dtype}")
-    _expect(out, "out", (T, H), like=z)
-    if residual is not None:
-        _expect(residual, "residual", (T, H), _dtype(out), like=z)
-    if weights is not None:
-        _expect(weights, "weights", (T, K), like=z)
-    with _On(z, stream) as s:
-        _check(lib().dpa_unpermute_rows(_dtype(z), _dptr(z), _dptr(pos), _dptr(weights),
-                                        -1 if weights is None else _dtype(weights), _dptr(residual), _dtype(out), T,
-                                        K, H, _dptr(out), s), "dpa_unpermute_rows")
+    dev, (T, K), H = _device(z), pos.shape, z.shape[-1]
+    out = _out(out, (T, H), z, residual, out_dtype, stream)
+    code, zcode, wcode = _float_type(out), _float_type(z), _real(weights)
+    _call(lib().dpa_unpermute_rows, "dpa_unpermute_rows", dev, stream, zcode,
+          _arg(z, "z", (T * K, H), zcode, dev), _arg(pos, "pos", (T, K), "int32", dev),
+          _opt(weights, "weights", (T, K), wcode, dev), wcode,
+          _opt(residual, "residual", (T, H), code, dev), code, T, K, H, _arg(out, "out", (T, H), code, dev))
     return out
+
+
+def _real(weights) -> int:
+    """DTYPE_* of gate weights (fp32 or fp64), -1 without weights."""
+    if weights is None:
+        return -1
+    code = _dtype(weights)
+    if code not in (DTYPE_FP32, DTYPE_FP64):
+        raise ValueError(f"weights: expected fp32 or fp64, got {weights.dtype}")
+    return code
 
 
 def unpermute_rows_backward(dy, z, pos, weights, dz=None, dweights=None, stream=None):
     """Gradients of unpermute_rows: (dz [T*K][H] in z's type, dweights fp32 [T][K]). dy: [T][H] of
     z's type. Rows of dz that no pair takes are left as they were (with dz=None: uninitialised);
     pairs that are not routed get dweights 0. The residual's gradient is dy itself."""
-    import torch
-    T, K = pos.shape
-    P, H = z.shape
-    _expect(pos, "pos", (T, K), torch.int32, like=z)
-    _expect(z, "z", (T * K, H))
-    _expect(dy, "dy", (T, H), _dtype(z), like=z)
-    _expect(weights, "weights", (T, K), like=z)
+    dev, (T, K), H = _device(z), pos.shape, z.shape[-1]
+    code, wcode = _float_type(z), _real(weights)
+    if weights is None:
+        raise ValueError("weights: expected a tensor")
     if dz is None:
-        dz = torch.empty_like(z)
+        dz = _new(z, z.shape, z.dtype, stream)
     if dweights is None:
-        dweights = torch.empty((T, K), dtype=torch.float32, device=z.device)
-    _expect(dz, "dz", (T * K, H), _dtype(z), like=z)
-    _expect(dweights, "dweights", (T, K), torch.float32, like=z)
-    with _On(z, stream) as s:
-        _check(lib().dpa_unpermute_rows_backward(_dtype(z), _dptr(dy), _dptr(z), _dptr(pos), _dptr(weights),
-                                                 _dtype(weights), T, K, H, _dptr(dz), _dptr(dweights), s),
-               "dpa_unpermute_rows_backward")
+        import torch
+        dweights = _new(z, (T, K), torch.float32, stream)
+    _call(lib().dpa_unpermute_rows_backward, "dpa_unpermute_rows_backward", dev, stream, code,
+          _arg(dy, "dy", (T, H), code, dev), _arg(z, "z", (T * K, H), code, dev),
+          _arg(pos, "pos", (T, K), "int32", dev), _arg(weights, "weights", (T, K), wcode, dev), wcode, T, K, H,
+          _arg(dz, "dz", (T * K, H), code, dev), _arg(dweights, "dweights", (T, K), DTYPE_FP32, dev))
     return dz, dweights
 
 
-def _product(call, name, x, w, lead, ws, bias, act, w_mul, bias_mul, residual, out, out_dtype, stream):
-    """Shared argument handling of linear and grouped_linear; `lead` is () or (n_groups,)."""
-    import torch
-    rows, K = x.shape
-    N = w.shape[-2]
-    dt = _dtype(x)
-    _expect(w, "w", (*lead, N, K), dt, like=x)
-    for t, what, shape in ((bias, "bias", (*lead, N)), (w_mul, "w_mul", (*lead, N, K)),
-                           (bias_mul, "bias_mul", (*lead, N))):
-        if t is not None:
-            _expect(t, what, shape, dt, like=x)
-    if out is None:
-        odt = out_dtype or (x.dtype if residual is None else residual.dtype)
-        out = torch.empty((rows, N), dtype=odt, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError(f"out: unexpected element type {out.dtype}")
-    _expect(out, "out", (rows, N), like=x)
-    if residual is not None:
-        _expect(residual, "residual", (rows, N), _dtype(out), like=x)
-    _expect(ws, "ws", ws.shape, torch.uint8, like=x)
+def _product(x, w, lead, bias, act, w_mul, bias_mul, residual, out, out_dtype, dev, stream):
+    """Arguments of linear and grouped_linear (`lead` is () or (n_groups,)): the descriptor, the
+    pointers of w, bias, w_mul, bias_mul, residual and out, and out."""
+    (rows, K), N, code = x.shape, w.shape[-2], _float_type(x)
+    out = _out(out, (rows, N), x, residual, out_dtype, stream)
+    ocode, wide, flat = _float_type(out), lead + (N, K), lead + (N,)
     if act not in ACTS:
         raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
-    desc = LinearDesc(rows, K, N, dt, _dtype(out), ACTS[act])
-    with _On(x, stream) as s:
-        _check(call(desc, _dptr(bias), _dptr(w_mul), _dptr(bias_mul), _dptr(residual), _dptr(out), s), name)
-    return out
+    ptrs = (_arg(w, "w", wide, code, dev), _opt(bias, "bias", flat, code, dev), _opt(w_mul, "w_mul", wide, code, dev),
+            _opt(bias_mul, "bias_mul", flat, code, dev), _opt(residual, "residual", (rows, N), ocode, dev),
+            _arg(out, "out", (rows, N), ocode, dev))
+    return ctypes.byref(LinearDesc(rows, K, N, code, ocode, ACTS[act])), ptrs, out
 
 
 def linear(x, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=None, out=None, out_dtype=None,
@@ -561,9 +577,11 @@ def linear(x, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=
     residual: [M][N] in x's type or fp32 (out_dtype; default: residual's, else x's); residual may be
     `out`. act: "none", "relu", "gelu", "gelu_tanh" or "silu". ws: new_linear_workspace or any
     other workspace; it receives the device error flag."""
-    return _product(lambda d, b, u, c, r, o, s: lib().dpa_linear(ctypes.byref(d), _dptr(x), _dptr(w), b, u, c, r, o,
-                                                                 _dptr(ws), ws.numel(), s),
-                    "dpa_linear", x, w, (), ws, bias, act, w_mul, bias_mul, residual, out, out_dtype, stream)
+    dev = _device(x)
+    desc, ptrs, out = _product(x, w, (), bias, act, w_mul, bias_mul, residual, out, out_dtype, dev, stream)
+    _call(lib().dpa_linear, "dpa_linear", dev, stream, desc, _arg(x, "x", x.shape, _dtype(x), dev), *ptrs,
+          _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
+    return out
 
 
 def grouped_linear(x, offsets, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=None, out=None,
@@ -572,13 +590,11 @@ def grouped_linear(x, offsets, w, ws, bias=None, act="none", w_mul=None, bias_mu
     take w[e]. offsets: int32 [E + 1] on the device (sort_pairs); w, w_mul: [E][N][K]; bias,
     bias_mul: [E][N]. Rows behind offsets[E] are neither used nor written (with out=None:
     uninitialised)."""
-    import torch
-    E = w.shape[0]
-    _expect(offsets, "offsets", (E + 1,), torch.int32, like=x)
-    return _product(lambda d, b, u, c, r, o, s: lib().dpa_grouped_linear(ctypes.byref(d), E, _dptr(x), _dptr(offsets),
-                                                                         _dptr(w), b, u, c, r, o, _dptr(ws),
-                                                                         ws.numel(), s),
-                    "dpa_grouped_linear", x, w, (E,), ws, bias, act, w_mul, bias_mul, residual, out, out_dtype, stream)
+    dev, E = _device(x), w.shape[0]
+    desc, ptrs, out = _product(x, w, (E,), bias, act, w_mul, bias_mul, residual, out, out_dtype, dev, stream)
+    _call(lib().dpa_grouped_linear, "dpa_grouped_linear", dev, stream, desc, E, _arg(x, "x", x.shape, _dtype(x), dev),
+          _arg(offsets, "offsets", (E + 1,), "int32", dev), *ptrs, _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
+    return out
 
 
 def stream_prefixes(desc: LayerDesc, host_planes, host_meta, experts, kplanes, dev_planes, dev_meta,
