@@ -19,8 +19,9 @@
 //           memory, and each then adds up its share of the outputs over the cluster, in rank
 //           order (deterministic), before the epilogue.
 //
-// Roles (320 threads): warps 0-7 epilogue (two per TMEM lane quadrant), warp 8 TMA loads (no
-// multicast), warp 9 TMEM allocation and MMA issue. Two accumulators of 256 columns alternate, so
+// Roles (576 threads): warps 0-15 epilogue (four per TMEM lane quadrant; with eight, an epilogue of
+// 256 tokens took longer than 2048 inputs' MMAs), warp 16 TMA loads (no multicast), warp 17 TMEM
+// allocation and MMA issue. Two accumulators of 256 columns alternate, so
 // a tile's epilogue overlaps the next tile's MMAs. Every wait is bounded: on a timeout the kernel
 // records DPA_ERR_DEVICE_TIMEOUT and every role leaves its loop.
 #include <cuda_bf16.h>
@@ -37,18 +38,28 @@ namespace {
 constexpr int kRowsA = 128;                      // weight rows per CTA (TMEM lanes)
 constexpr int kStepK = 64;                       // K per stage: one 128-byte swizzle row of 16-bit values
 constexpr int kATile = kRowsA * 128;             // 16 KB
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16, kGroups = kEpiWarps / 4;   // a group is one warp per TMEM lane quadrant
+constexpr int kChunk = 16;                       // tokens that a group finishes at a time
 constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kThreads = (kEpiWarps + 2) * 32;   // 320
+constexpr int kThreads = (kEpiWarps + 2) * 32;   // 576
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512, kAccCols = 256;
 constexpr int kSmemMax = 232448;
-constexpr int kOutBytes = 2 * 32 * kRowsA * 4;   // epilogue staging, one 32-token chunk per half
+constexpr int kOutBytes = kGroups * kChunk * kRowsA * 4;   // epilogue staging, one chunk per group
 // full[stages], empty[stages], acc_full[2], acc_empty[2], done; then the TMEM address and abort flag
 constexpr int kBarBytes = (2 * kMaxStages + 5) * 8 + 16;
 
 struct Tile {
     int e, row0, n, ft;
+};
+
+// Maps of x for one load per stage: plain, boxes of a whole tile's rows (the first map); grouped,
+// boxes of 16, 32, 64 and 128 rows, of which a tile takes the smallest that holds its rows. (Several
+// boxes of 32 rows per stage cost more than the rows that a larger box reads in vain: 128 experts of
+// 256 rows 218 against 196 us.)
+constexpr int kRowMaps = 4;
+struct RowMaps {
+    CUtensorMap m[kRowMaps];
 };
 
 // Rows of one token tile when n rows are cut into tiles of at most tn: equal parts rounded up to
@@ -164,8 +175,8 @@ __device__ __forceinline__ void store_out(const LinearArgs& a, const float (&v)[
     }
 }
 
-// Barrier of the four warps of an epilogue half; `ok` comes back false if any of them brought false.
-__device__ __forceinline__ bool half_agree(int half, bool ok) {
+// Barrier of the four warps of an epilogue group; `ok` comes back false if any of them brought false.
+__device__ __forceinline__ bool group_agree(int grp, bool ok) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -173,12 +184,12 @@ __device__ __forceinline__ bool half_agree(int half, bool ok) {
         "barrier.cta.red.and.aligned.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(ok)), "r"(1 + half)
+        : "r"(static_cast<uint32_t>(ok)), "r"(1 + grp)
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void half_sync(int half) {
-    asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + half) : "memory");
+__device__ __forceinline__ void group_sync(int grp) {
+    asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + grp) : "memory");
 }
 
 // ---- pair (cta_group::2) forms of the tensor-core operations ----
@@ -241,7 +252,7 @@ __device__ __forceinline__ void load3d(void* dst, const CUtensorMap* map, int x,
             : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -255,7 +266,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 template <int CG, bool GATED, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ CUtensorMap umap,
-                                                             const __grid_constant__ CUtensorMap xmap) {
+                                                             const __grid_constant__ RowMaps xmaps) {
     constexpr int kFeat = GATED ? 64 : 128;   // output features per CTA
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -263,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     const int stages = a.stages, btile = (a.TN / CG) * 128;
     unsigned char* sA = sm;
     unsigned char* sB = sm + stages * kATile;
-    float* s_out = reinterpret_cast<float*>(sB + stages * btile);   // [2][32 tokens][128] epilogue staging
+    float* s_out = reinterpret_cast<float*>(sB + stages * btile);   // [kGroups][kChunk][128] epilogue staging
     unsigned char* tail = sB + stages * btile + kOutBytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(tail);
     uint64_t* empty = full + kMaxStages;
@@ -352,10 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             for (int64_t it = cid; it < ntiles && ok; it += ncl) {
                 const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
                 const int part = ((t.n + 16 * CG - 1) / (16 * CG)) * 16;   // token rows of this CTA
-                const int nbox = (part + a.xbox - 1) / a.xbox;
+                int mi = 0, box = a.xbox;
+                while (box < part) {   // grouped only: a plain tile's box holds it
+                    box *= 2;
+                    ++mi;
+                }
                 const int f0 = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat;
                 const int r0 = t.row0 + (CG == 2 ? rank * part : 0);
-                const uint32_t bytes = static_cast<uint32_t>(CG) * (kATile + nbox * a.xbox * 128);
+                const uint32_t bytes = static_cast<uint32_t>(CG) * (kATile + box * 128);
                 for (int kc = k0; kc < k1; ++kc) {
                     if (!mbar_wait_abortable(&empty[s], ph, s_abort, a.hdr, 0x710)) {
                         ok = false;
@@ -371,9 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                     } else {
                         load3d<CG>(da, &wmap, kc * kStepK, f0, t.e, bar);
                     }
-                    unsigned char* db = sB + s * btile;
-                    for (int i = 0; i < nbox; ++i)
-                        load2d<CG>(db + i * a.xbox * 128, &xmap, kc * kStepK, r0 + i * a.xbox, bar);
+                    load2d<CG>(sB + s * btile, &xmaps.m[mi], kc * kStepK, r0, bar);
                     if (++s == stages) {
                         s = 0;
                         ph ^= 1;
@@ -434,19 +447,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         }
     } else {
         // ================= epilogue =================
-        // The four warps of a half take every second 32-token chunk. A chunk is read from TMEM
+        // The four warps of a group take every fourth chunk of 16 tokens. A chunk is read from TMEM
         // (lane = weight row) and turned through shared memory, so that each thread then finishes 8
         // consecutive features of a token and a token's features leave as one contiguous run. The
         // staging columns are permuted (kept in place within a 16-byte piece) so that both sides
         // are free of bank conflicts.
-        const int q = warp & 3, half = warp >> 2, R = 32 * q + lane;
+        const int q = warp & 3, grp = warp >> 2, R = 32 * q + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-        float* stage = s_out + half * (32 * kRowsA);
+        float* stage = s_out + grp * (kChunk * kRowsA);
         float* put = stage + (R ^ ((q & 1) * 4 + (q >> 1) * 16));
         // this thread's features and tokens of a chunk
-        constexpr int kGroups = kFeat / 8, kItems = 32 * kGroups / 128, kTokStep = 32 / kItems;
-        const int ht = R;   // thread of the half
-        const int fg = ht % kGroups, tk0 = ht / kGroups;
+        constexpr int kFeatGroups = kFeat / 8, kItems = kChunk * kFeatGroups / 128, kTokStep = kChunk / kItems;
+        const int fg = R % kFeatGroups, tk0 = R / kFeatGroups;   // R is also the thread of the group
         const int R0 = fg * 8, qr = R0 >> 5;
         const int sw = (qr & 1) * 4 + (qr >> 1) * 16;
         const float* get0 = stage + (R0 ^ sw);
@@ -465,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             const int b = j & 1;
             const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + fg * 8;
             const int cnt = min(max(a.N - f, 0), 8);
-            const int nch = (t.n + 31) >> 5;
+            const int nch = (t.n + kChunk - 1) / kChunk;
             float bias[8], bmul[8];
             Out8 res[kItems];
             if (CG == 2 || S == 1) {   // operands of the epilogue: loaded while the MMAs run
@@ -478,35 +490,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                 if (a.residual && cnt > 0) {
 #pragma unroll
                     for (int i = 0; i < kItems; ++i) {
-                        const int tok = 32 * half + tk0 + i * kTokStep;
+                        const int tok = kChunk * grp + tk0 + i * kTokStep;
                         if (tok < t.n)
                             res[i] = load_residual(a, (static_cast<int64_t>(t.row0) + tok) * a.N + f, vec, cnt);
                     }
                 }
             }
             bool w_ok = mbar_wait_abortable(&acc_full[b], (j >> 1) & 1, s_abort, a.hdr, 0x730);
-            w_ok = half_agree(half, w_ok);   // the half leaves together (it synchronises below)
+            w_ok = group_agree(grp, w_ok);   // the group leaves together (it synchronises below)
             if (!w_ok) break;
             tc_fence_after();
             const uint32_t acc = tmem + lane_base + static_cast<uint32_t>(b) * kAccCols;
             if (CG == 1 && S > 1) {
                 // partial sums [token][128] into the (now idle) stage memory
                 float* part = reinterpret_cast<float*>(sm);
-                for (int c = half; c < nch; c += 2) {
-                    uint32_t v[32];
-                    tmem_ld32(acc + 32 * c, v);
+                for (int c = grp; c < nch; c += kGroups) {
+                    uint32_t v[kChunk];
+                    tmem_ld16(acc + kChunk * c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 32; ++u)
-                        if (32 * c + u < t.n) part[(32 * c + u) * kRowsA + R] = __uint_as_float(v[u]);
+                    for (int u = 0; u < kChunk; ++u)
+                        if (kChunk * c + u < t.n) part[(kChunk * c + u) * kRowsA + R] = __uint_as_float(v[u]);
                 }
                 break;   // one tile per cluster
             }
-            for (int c = half; c < nch; c += 2) {
-                uint32_t v[32];
-                tmem_ld32(acc + 32 * c, v);
+            for (int c = grp; c < nch; c += kGroups) {
+                uint32_t v[kChunk];
+                tmem_ld16(acc + kChunk * c, v);
                 tmem_wait_ld();
-                if (c + 2 >= nch) {   // last read of this accumulator by this warp
+                if (c + kGroups >= nch) {   // last read of this accumulator by this warp
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -514,14 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                         else mbarrier_arrive(&acc_empty[b]);
                     }
                 }
-                if (c > half) half_sync(half);   // the chunk before has been read out
+                if (c > grp) group_sync(grp);   // the chunk before has been read out
 #pragma unroll
-                for (int u = 0; u < 32; ++u) put[u * kRowsA] = __uint_as_float(v[u]);
-                half_sync(half);
+                for (int u = 0; u < kChunk; ++u) put[u * kRowsA] = __uint_as_float(v[u]);
+                group_sync(grp);
                 if (cnt > 0) {
 #pragma unroll
                     for (int i = 0; i < kItems; ++i) {
-                        const int in = tk0 + i * kTokStep, tok = 32 * c + in;
+                        const int in = tk0 + i * kTokStep, tok = kChunk * c + in;
                         if (tok >= t.n) break;
                         const int64_t at = (static_cast<int64_t>(t.row0) + tok) * a.N + f;
                         const float4 x0 = *reinterpret_cast<const float4*>(get0 + in * kRowsA);
@@ -539,19 +551,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                         }
                         if (a.residual) {
                             add_residual<F16>(a, res[i], g);
-                            if (tok + 64 < t.n) res[i] = load_residual(a, at + 64 * static_cast<int64_t>(a.N), vec, cnt);
+                            if (tok + kChunk * kGroups < t.n)
+                                res[i] = load_residual(a, at + kChunk * kGroups * static_cast<int64_t>(a.N), vec, cnt);
                         }
                         store_out<F16>(a, g, at, vec, cnt);
                     }
                 }
             }
-            if (half >= nch) {   // this half had nothing to read
+            if (grp >= nch) {   // this group had nothing to read
                 if (lane == 0) {
                     if (CG == 2) arrive_cluster(empty_bar[b]);
                     else mbarrier_arrive(&acc_empty[b]);
                 }
             }
-            half_sync(half);   // read out before the next tile is staged
+            group_sync(grp);   // read out before the next tile is staged
         }
     }
     __syncwarp();
@@ -626,7 +639,8 @@ bool encode_map(CUtensorMap* map, const void* base, bool f16, uint64_t cols, uin
 }
 
 template <int CG, bool GATED, bool F16>
-cudaError_t launch_variant(LinearArgs& a, const CUtensorMap* maps, int clusters, size_t smem, cudaStream_t stream) {
+cudaError_t launch_variant(LinearArgs& a, const CUtensorMap* wmaps, const RowMaps& xmaps, int clusters, size_t smem,
+                           cudaStream_t stream) {
     const void* fn = reinterpret_cast<const void*>(linear_kernel<CG, GATED, F16>);
     const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (err != cudaSuccess) return err;
@@ -645,8 +659,7 @@ cudaError_t launch_variant(LinearArgs& a, const CUtensorMap* maps, int clusters,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = csize > 1 ? 2 : 1;
-    alignas(64) CUtensorMap m0 = maps[0], m1 = maps[1], m2 = maps[2];
-    void* args[] = {&a, &m0, &m1, &m2};
+    void* args[] = {&a, const_cast<CUtensorMap*>(wmaps), const_cast<CUtensorMap*>(wmaps + 1), const_cast<RowMaps*>(&xmaps)};
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
@@ -670,7 +683,7 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
     int64_t clusters;
     if (a.E > 0) {
         a.TN = pair ? 256 : 128;
-        a.xbox = mean >= 32 ? 32 : 16;
+        a.xbox = 16;
         // most token tiles there can be: every full tile, and one more per non-empty group
         const int64_t tiles =
             (static_cast<int64_t>(a.rows) / a.TN + (a.rows < a.E ? a.rows : a.E)) * a.FT;
@@ -691,24 +704,27 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
     a.stages = (kSmemMax - fixed) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const size_t smem = static_cast<size_t>(a.stages) * stage + fixed;
-    alignas(64) CUtensorMap maps[3];
+    alignas(64) CUtensorMap maps[2];
+    alignas(64) RowMaps xmaps;
     const uint64_t E = static_cast<uint64_t>(groups);
     const uint32_t wbox = static_cast<uint32_t>(feat);
     if (!encode_map(&maps[0], w, f16, a.K, a.N, E, wbox, 3) ||
-        !encode_map(&maps[1], gated ? w_mul : w, f16, a.K, a.N, E, wbox, 3) ||
-        !encode_map(&maps[2], x, f16, a.K, a.rows, 1, static_cast<uint32_t>(a.xbox), 2))
+        !encode_map(&maps[1], gated ? w_mul : w, f16, a.K, a.N, E, wbox, 3))
         return cudaErrorInvalidValue;
+    for (int i = 0; i < kRowMaps; ++i)
+        if (!encode_map(&xmaps.m[i], x, f16, a.K, a.rows, 1, static_cast<uint32_t>(a.E > 0 ? a.xbox << i : a.xbox), 2))
+            return cudaErrorInvalidValue;
     const int c = static_cast<int>(clusters);
     if (pair) {
-        if (gated) return f16 ? launch_variant<2, true, true>(a, maps, c, smem, stream)
-                              : launch_variant<2, true, false>(a, maps, c, smem, stream);
-        return f16 ? launch_variant<2, false, true>(a, maps, c, smem, stream)
-                   : launch_variant<2, false, false>(a, maps, c, smem, stream);
+        if (gated) return f16 ? launch_variant<2, true, true>(a, maps, xmaps, c, smem, stream)
+                              : launch_variant<2, true, false>(a, maps, xmaps, c, smem, stream);
+        return f16 ? launch_variant<2, false, true>(a, maps, xmaps, c, smem, stream)
+                   : launch_variant<2, false, false>(a, maps, xmaps, c, smem, stream);
     }
-    if (gated) return f16 ? launch_variant<1, true, true>(a, maps, c, smem, stream)
-                          : launch_variant<1, true, false>(a, maps, c, smem, stream);
-    return f16 ? launch_variant<1, false, true>(a, maps, c, smem, stream)
-               : launch_variant<1, false, false>(a, maps, c, smem, stream);
+    if (gated) return f16 ? launch_variant<1, true, true>(a, maps, xmaps, c, smem, stream)
+                          : launch_variant<1, true, false>(a, maps, xmaps, c, smem, stream);
+    return f16 ? launch_variant<1, false, true>(a, maps, xmaps, c, smem, stream)
+               : launch_variant<1, false, false>(a, maps, xmaps, c, smem, stream);
 }
 
 }  // namespace dpa
