@@ -277,7 +277,7 @@ struct LinearArgs {
     int act, out32;           // DPA_ACT_*; 1: fp32 output
     WsHeader* hdr;
     // set by the launcher: K steps, feature tiles, most tokens per tile, CTAs sharing K, pipeline
-    // stages, rows per token load
+    // stages, rows of the smallest token load
     int ksteps, FT, TN, splits, stages, xbox;
 };
 cudaError_t launch_linear(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,

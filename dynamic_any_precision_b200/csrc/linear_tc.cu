@@ -164,8 +164,7 @@ __device__ __forceinline__ void store_out(const LinearArgs& a, const float (&v)[
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[i] = static_cast<uint32_t>(down16<F16>(v[2 * i])) |
-                       static_cast<uint32_t>(down16<F16>(v[2 * i + 1])) << 16;
+                w[i] = down16x2<F16>(v[2 * i], v[2 * i + 1]);
             *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
@@ -222,32 +221,32 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 // tensor loads into this CTA's shared memory, completing on `bar` (shared::cluster address; of the
 // pair's first CTA with CG = 2)
 template <int CG>
-__device__ __forceinline__ void load2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void load2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     if constexpr (CG == 1)
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
             : "memory");
 }
 template <int CG>
-__device__ __forceinline__ void load3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void load3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     if constexpr (CG == 1)
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
 }
@@ -356,8 +355,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     const int k1 = CG == 1 ? static_cast<int>(static_cast<int64_t>(a.ksteps) * (rank + 1) / S) : a.ksteps;
 
     if (warp == kLoadWarp) {
-        // ================= loads: one lane =================
-        if (lane == 0) {
+        // ================= loads =================
+        // The whole warp runs the loop, so that its counters and addresses stay in uniform registers,
+        // and one elected lane issues the copies (as a loop of one lane, the issue bound the kernel).
+        {
+            const bool leader = elect_one();
+            const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
+            const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
             int s = 0, ph = 1;
             bool ok = true;
             for (int64_t it = cid; it < ntiles && ok; it += ncl) {
@@ -368,25 +372,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                     box *= 2;
                     ++mi;
                 }
+                const CUtensorMap* xm = &xmaps.m[mi];
                 const int f0 = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat;
                 const int r0 = t.row0 + (CG == 2 ? rank * part : 0);
                 const uint32_t bytes = static_cast<uint32_t>(CG) * (kATile + box * 128);
                 for (int kc = k0; kc < k1; ++kc) {
-                    if (!mbar_wait_abortable(&empty[s], ph, s_abort, a.hdr, 0x710)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_abortable(&empty[s], ph, s_abort, a.hdr, 0x710))) {
                         ok = false;
                         break;
                     }
-                    uint32_t bar = smem_u32(&full[s]);
-                    if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-                    if (CG == 2) bar = mapa_shared(bar, 0);
-                    unsigned char* da = sA + s * kATile;
-                    if constexpr (GATED) {
+                    if (leader) {
+                        const uint32_t bar = full0 + 8 * s, da = a0 + s * kATile;
+                        if (CG == 1 || rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                         load3d<CG>(da, &wmap, kc * kStepK, f0, t.e, bar);
-                        load3d<CG>(da + kATile / 2, &umap, kc * kStepK, f0, t.e, bar);
-                    } else {
-                        load3d<CG>(da, &wmap, kc * kStepK, f0, t.e, bar);
+                        if constexpr (GATED) load3d<CG>(da + kATile / 2, &umap, kc * kStepK, f0, t.e, bar);
+                        load2d<CG>(b0 + s * btile, xm, kc * kStepK, r0, bar);
                     }
-                    load2d<CG>(sB + s * btile, &xmaps.m[mi], kc * kStepK, r0, bar);
+                    __syncwarp();
                     if (++s == stages) {
                         s = 0;
                         ph ^= 1;
@@ -478,14 +480,17 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + fg * 8;
             const int cnt = min(max(a.N - f, 0), 8);
             const int nch = (t.n + kChunk - 1) / kChunk;
-            float bias[8], bmul[8];
+            Two bias[4], bmul[4];
             Out8 res[kItems];
             if (CG == 2 || S == 1) {   // operands of the epilogue: loaded while the MMAs run
                 const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    bias[i] = i < cnt ? bias_at<F16>(a.bias, fb + i) : 0.f;
-                    bmul[i] = GATED && i < cnt ? bias_at<F16>(a.bias_mul, fb + i) : 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const bool in0 = 2 * i < cnt, in1 = 2 * i + 1 < cnt;
+                    bias[i] = two(in0 ? bias_at<F16>(a.bias, fb + 2 * i) : 0.f, in1 ? bias_at<F16>(a.bias, fb + 2 * i + 1) : 0.f);
+                    if (GATED)
+                        bmul[i] = two(in0 ? bias_at<F16>(a.bias_mul, fb + 2 * i) : 0.f,
+                                      in1 ? bias_at<F16>(a.bias_mul, fb + 2 * i + 1) : 0.f);
                 }
                 if (a.residual && cnt > 0) {
 #pragma unroll
@@ -538,16 +543,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                         const int64_t at = (static_cast<int64_t>(t.row0) + tok) * a.N + f;
                         const float4 x0 = *reinterpret_cast<const float4*>(get0 + in * kRowsA);
                         const float4 x1 = *reinterpret_cast<const float4*>(get1 + in * kRowsA);
-                        float g[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                        Two g2[4] = {two(x0.x, x0.y), two(x0.z, x0.w), two(x1.x, x1.y), two(x1.z, x1.w)};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) g[e] += bias[e];
-                        act_many(g, a.act);
+                        for (int e = 0; e < 4; ++e) g2[e] = add2(g2[e], bias[e]);
+                        act_many(g2, a.act);
                         if constexpr (GATED) {
                             const float4 m0 = *reinterpret_cast<const float4*>(gum0 + in * kRowsA);
                             const float4 m1 = *reinterpret_cast<const float4*>(gum1 + in * kRowsA);
-                            const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+                            const Two m[4] = {two(m0.x, m0.y), two(m0.z, m0.w), two(m1.x, m1.y), two(m1.z, m1.w)};
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) g[e] *= m[e] + bmul[e];
+                            for (int e = 0; e < 4; ++e) g2[e] = mul2(g2[e], add2(m[e], bmul[e]));
+                        }
+                        float g[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 h = apart(g2[e]);
+                            g[2 * e] = h.x;
+                            g[2 * e + 1] = h.y;
                         }
                         if (a.residual) {
                             add_residual<F16>(a, res[i], g);
