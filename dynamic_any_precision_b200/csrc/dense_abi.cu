@@ -44,6 +44,7 @@ dpa_status run_linear(const dpa_linear_desc* d, int groups, const void* x, const
     if (!d || d->rows <= 0 || d->in_features <= 0 || d->out_features <= 0) return DPA_ERR_INVALID_ARG;
     if (d->dtype != DPA_DTYPE_BF16 && d->dtype != DPA_DTYPE_FP16) return DPA_ERR_INVALID_ARG;
     if (d->out_dtype != d->dtype && d->out_dtype != DPA_DTYPE_FP32) return DPA_ERR_INVALID_ARG;
+    if (residual && d->residual_dtype != d->out_dtype && d->residual_dtype != DPA_DTYPE_FP32) return DPA_ERR_INVALID_ARG;
     if (d->act < DPA_ACT_NONE || d->act > DPA_ACT_SILU) return DPA_ERR_INVALID_ARG;
     if (!given16(x) || !given16(w) || !given16(out) || !given16(ws)) return DPA_ERR_INVALID_ARG;
     if (!opt16(bias) || !opt16(w_mul) || !opt16(bias_mul) || !opt16(residual)) return DPA_ERR_INVALID_ARG;
@@ -62,6 +63,7 @@ dpa_status run_linear(const dpa_linear_desc* d, int groups, const void* x, const
     a.out = out;
     a.act = d->act;
     a.out32 = d->out_dtype == DPA_DTYPE_FP32;
+    a.res32 = d->residual_dtype == DPA_DTYPE_FP32;
     a.hdr = static_cast<dpa::WsHeader*>(ws);
     return launched(dpa::launch_linear(a, d->dtype == DPA_DTYPE_FP16, x, w, w_mul, static_cast<cudaStream_t>(stream),
                                        sms_current()));
@@ -106,12 +108,13 @@ dpa_status dpa_permute_rows(int dtype, const void* x, const int32_t* pos, int n_
 }
 
 dpa_status dpa_unpermute_rows(int dtype, const void* z, const int32_t* pos, const void* weights, int weight_dtype,
-                              const void* residual, int out_dtype, int n_tokens, int top_k, int hidden, void* y,
-                              void* stream) {
+                              const void* residual, int residual_dtype, int out_dtype, int n_tokens, int top_k,
+                              int hidden, void* y, void* stream) {
     const dpa_status st = check_rows(n_tokens, top_k, hidden);
     if (st != DPA_OK) return st;
     if (!row_type(dtype) || !row_type(out_dtype)) return DPA_ERR_INVALID_ARG;
     if (dtype != out_dtype && dtype != DPA_DTYPE_FP32 && out_dtype != DPA_DTYPE_FP32) return DPA_ERR_INVALID_ARG;
+    if (residual && residual_dtype != out_dtype && residual_dtype != DPA_DTYPE_FP32) return DPA_ERR_INVALID_ARG;
     if (!given16(z) || !given16(pos) || !given16(y) || !opt16(residual) || !check_weights(weights, weight_dtype))
         return DPA_ERR_INVALID_ARG;
     dpa::UnpermuteArgs a{};
@@ -124,7 +127,8 @@ dpa_status dpa_unpermute_rows(int dtype, const void* z, const int32_t* pos, cons
     a.T = n_tokens;
     a.K = top_k;
     a.H = hidden;
-    return launched(dpa::launch_unpermute(a, dtype, out_dtype, static_cast<cudaStream_t>(stream), sms_current()));
+    return launched(dpa::launch_unpermute(a, dtype, out_dtype, residual_dtype == DPA_DTYPE_FP32,
+                                          static_cast<cudaStream_t>(stream), sms_current()));
 }
 
 dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z, const int32_t* pos,

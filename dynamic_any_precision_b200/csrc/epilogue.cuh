@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "kernels.h"
 
 namespace dpa {
 
@@ -160,6 +161,16 @@ __device__ __forceinline__ uint32_t down16x2(float lo, float hi) {
 template <bool F16>
 __device__ __forceinline__ float bias_at(const void* b, int64_t i) {
     return b ? up16<F16>(__ldg(static_cast<const uint16_t*>(b) + i)) : 0.f;
+}
+
+// One output: adds its residual, rounds once and stores it (`out` may be the residual itself).
+template <bool F16>
+__device__ __forceinline__ void store_one(const LinearArgs& a, float o, int64_t at) {
+    if (a.residual)
+        o += a.res32 ? static_cast<const float*>(a.residual)[at]
+                     : up16<F16>(static_cast<const uint16_t*>(a.residual)[at]);
+    if (a.out32) static_cast<float*>(a.out)[at] = o;
+    else static_cast<uint16_t*>(a.out)[at] = down16<F16>(o);
 }
 
 }  // namespace dpa

@@ -247,11 +247,11 @@ struct UnpermuteArgs {
     const int32_t* pos;       // [T][K]
     const void* weights;      // [T][K] fp32 or fp64, or nullptr (all 1)
     int wtype;                // DPA_DTYPE_FP32, DPA_DTYPE_FP64, or -1 without weights
-    const void* residual;     // [T][H] in y's type, or nullptr
+    const void* residual;     // [T][H] in y's type or fp32, or nullptr
     void* y;                  // [T][H]
     int T, K, H;
 };
-cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, cudaStream_t stream, int sms);
+cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, bool res32, cudaStream_t stream, int sms);
 
 struct UnpermuteBwdArgs {
     const void* dy;           // [T][H]
@@ -272,9 +272,9 @@ struct LinearArgs {
     const int32_t* offsets;   // [E + 1] first row of each group
     const void* bias;         // [N] or [E][N], or nullptr
     const void* bias_mul;     // the same for the second product, or nullptr
-    const void* residual;     // [rows][N] in the output's type, or nullptr
+    const void* residual;     // [rows][N] in the output's type or fp32, or nullptr
     void* out;                // [rows][N]
-    int act, out32;           // DPA_ACT_*; 1: fp32 output
+    int act, out32, res32;    // DPA_ACT_*; 1: fp32 output, fp32 residual
     WsHeader* hdr;
     // set by the launcher: K steps, feature tiles, most tokens per tile, CTAs sharing K, pipeline
     // stages, rows of the smallest token load

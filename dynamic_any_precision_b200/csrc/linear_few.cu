@@ -114,13 +114,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(LinearArgs a, con
         float o = act_one(v[0] + bias_at<F16>(a.bias, f), a.act);
         if (MATS == 2) o *= v[MATS - 1] + bias_at<F16>(a.bias_mul, f);
         const int64_t at = static_cast<int64_t>(tok) * a.N + f;
-        if (a.out32) {
-            if (a.residual) o += static_cast<const float*>(a.residual)[at];
-            static_cast<float*>(a.out)[at] = o;
-        } else {
-            if (a.residual) o += up16<F16>(static_cast<const uint16_t*>(a.residual)[at]);
-            static_cast<uint16_t*>(a.out)[at] = down16<F16>(o);
-        }
+        store_one<F16>(a, o, at);
     }
 }
 

@@ -98,14 +98,14 @@ __device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref
     return t;
 }
 
-// Eight consecutive outputs of one token. `vec`: rows of whole 8-feature groups (N % 8 == 0, so that
+// Eight consecutive outputs (or residual values) of one token. `vec`: rows of whole 8-feature groups (N % 8 == 0, so that
 // every group is 16-byte aligned and wholly inside or outside N); otherwise `cnt` single elements.
 struct Out8 {
-    uint4 lo, hi;   // 16-bit outputs: lo only; fp32: lo, hi
+    uint4 lo, hi;   // 16-bit values: lo only; fp32: lo, hi
 };
 __device__ __forceinline__ Out8 load_residual(const LinearArgs& a, int64_t at, bool vec, int cnt) {
     Out8 r;
-    if (a.out32) {
+    if (a.res32) {
         const float* p = static_cast<const float*>(a.residual) + at;
         if (vec) {
             r.lo = *reinterpret_cast<const uint4*>(p);
@@ -134,7 +134,7 @@ __device__ __forceinline__ Out8 load_residual(const LinearArgs& a, int64_t at, b
 template <bool F16>
 __device__ __forceinline__ void add_residual(const LinearArgs& a, const Out8& r, float (&v)[8]) {
     const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
-    if (a.out32) {
+    if (a.res32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(w[i]);
     } else {
@@ -612,13 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                 float o = act_one(v + bias_at<F16>(a.bias, fb), a.act);
                 if (GATED) o *= m + bias_at<F16>(a.bias_mul, fb);
                 const int64_t at = (static_cast<int64_t>(t.row0) + tok) * a.N + f;
-                if (a.out32) {
-                    if (a.residual) o += static_cast<const float*>(a.residual)[at];
-                    static_cast<float*>(a.out)[at] = o;
-                } else {
-                    if (a.residual) o += up16<F16>(static_cast<const uint16_t*>(a.residual)[at]);
-                    static_cast<uint16_t*>(a.out)[at] = down16<F16>(o);
-                }
+                store_one<F16>(a, o, at);
             }
         }
         cluster_sync();   // no CTA leaves while another reads its partial sums

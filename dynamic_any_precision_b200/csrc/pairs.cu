@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(256) permute_kernel(const V* x, const int32_t*
 // rows of up to 8 slots are in flight together and are added in slot order in fp32. Weights in
 // fp64 are rounded to fp32 first (2^-24 relative, below the fp32 products' own rounding); the
 // result is rounded once.
-template <typename ZT, typename YT, int VEC>
+template <typename ZT, typename YT, typename RT, int VEC>
 __global__ void __launch_bounds__(256) unpermute_kernel(UnpermuteArgs a, int wpt) {
     constexpr int U = pieces(VEC);
     pdl_wait();
@@ -341,18 +341,18 @@ __global__ void __launch_bounds__(256) unpermute_kernel(UnpermuteArgs a, int wpt
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / wpt) + warp / wpt;
     if (t >= a.T) return;
     const Slots s = load_slots(a.pos, a.weights, a.wtype, t, a.K, static_cast<unsigned>(a.T) * a.K, lane);
-    const YT* res = a.residual ? static_cast<const YT*>(a.residual) + t * a.H : nullptr;
+    const RT* res = a.residual ? static_cast<const RT*>(a.residual) + t * a.H : nullptr;
     YT* yr = static_cast<YT*>(a.y) + t * a.H;
     for (int c0 = (warp % wpt) * (32 * VEC * U); c0 < a.H; c0 += wpt * (32 * VEC * U)) {   // the warp stays together
         int c[U];
         bool in[U];
-        Pack<YT, VEC> r[U];
+        Pack<RT, VEC> r[U];
         float acc[U][VEC];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             c[i] = c0 + (32 * i + lane) * VEC;
             in[i] = c[i] < a.H;
-            r[i] = load_if<YT, VEC>(res + c[i], res && in[i]);
+            r[i] = load_if<RT, VEC>(res + c[i], res && in[i]);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) acc[i][j] = 0.f;
         }
@@ -442,9 +442,9 @@ struct Cursor {
     }
 };
 
-template <typename ZT, typename YT>
+template <typename ZT, typename YT, typename RT>
 __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) unpermute_stream_kernel(UnpermuteArgs a, int runs) {
-    constexpr int VEC = 16 / sizeof(ZT), kRes = VEC * sizeof(YT);
+    constexpr int VEC = 16 / sizeof(ZT), kRes = VEC * sizeof(RT);
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_wait();
     const int lane = threadIdx.x & 31;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) unpermute_stream_
                 }
             }
             if (a.residual && in.s0 + kStreamRows >= in.n) {
-                const YT* rr = static_cast<const YT*>(a.residual) + in.t * a.H + c;
+                const RT* rr = static_cast<const RT*>(a.residual) + in.t * a.H + c;
 #pragma unroll
                 for (int i = 0; i < kStreamPieces; ++i)
                     if (c + i * 32 * VEC < a.H)
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) unpermute_stream_
             for (int i = 0; i < kStreamPieces; ++i) {
                 Pack<YT, VEC> y;
                 if (a.residual) {
-                    const Pack<YT, VEC> r = *reinterpret_cast<const Pack<YT, VEC>*>(
+                    const Pack<RT, VEC> r = *reinterpret_cast<const Pack<RT, VEC>*>(
                         src + kStreamRes + (i * kStreamThreads + threadIdx.x) * kRes);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) acc[i][j] = up(r.v[j]) + acc[i][j];
@@ -656,7 +656,7 @@ cudaError_t permute_vec(const void* x, const int32_t* pos, void* out, int T, int
     return launch_pdl_raw(fn, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, args);
 }
 
-template <typename ZT, typename YT>
+template <typename ZT, typename YT, typename RT>
 cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream, int sms) {
     constexpr int kWidest = sizeof(ZT) == 2 ? 8 : 4;
     const int vec = pack_of(a.H, kWidest);
@@ -668,7 +668,7 @@ cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream, int sms
     // two items per warp at least (1024 tokens of 8 rows of 2048 bf16: 7.5 us, against 8.9 us for the
     // kernel without the ring; 4096 tokens: 27 against 40 us)
     if (vec == kWidest && static_cast<int64_t>(a.T) * runs >= static_cast<int64_t>(ctas) * (kStreamThreads / 32) * 2) {
-        const void* fn = reinterpret_cast<const void*>(unpermute_stream_kernel<ZT, YT>);
+        const void* fn = reinterpret_cast<const void*>(unpermute_stream_kernel<ZT, YT, RT>);
         const size_t smem = static_cast<size_t>(kStreamStages) * kStreamStage;
         const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (err != cudaSuccess) return err;
@@ -677,11 +677,17 @@ cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream, int sms
         return launch_pdl_raw(fn, dim3(ctas), dim3(kStreamThreads), smem, stream, sargs);
     }
     void* args[] = {&b, &wpt};
-    const void* fn = vec == kWidest ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, kWidest>)
-                     : vec == 4     ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, 4>)
-                     : vec == 2     ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, 2>)
-                                    : reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, 1>);
+    const void* fn = vec == kWidest ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, RT, kWidest>)
+                     : vec == 4     ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, RT, 4>)
+                     : vec == 2     ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, RT, 2>)
+                                    : reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, RT, 1>);
     return launch_pdl_raw(fn, dim3((a.T - 1) / (8 / wpt) + 1), dim3(256), 0, stream, args);
+}
+
+// the residual has y's type or is fp32
+template <typename ZT, typename YT>
+cudaError_t unpermute_residual(const UnpermuteArgs& a, bool res32, cudaStream_t stream, int sms) {
+    return res32 ? unpermute_types<ZT, YT, float>(a, stream, sms) : unpermute_types<ZT, YT, YT>(a, stream, sms);
 }
 
 template <typename T>
@@ -756,14 +762,14 @@ cudaError_t launch_permute_pairs(int elem_bytes, const void* x, const int32_t* p
     }
 }
 
-cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, cudaStream_t stream, int sms) {
-    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_BF16) return unpermute_types<__nv_bfloat16, __nv_bfloat16>(a, stream, sms);
-    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP16) return unpermute_types<__half, __half>(a, stream, sms);
-    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP32) return unpermute_types<float, float>(a, stream, sms);
-    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_FP32) return unpermute_types<__nv_bfloat16, float>(a, stream, sms);
-    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP32) return unpermute_types<__half, float>(a, stream, sms);
-    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_BF16) return unpermute_types<float, __nv_bfloat16>(a, stream, sms);
-    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP16) return unpermute_types<float, __half>(a, stream, sms);
+cudaError_t launch_unpermute(const UnpermuteArgs& a, int ztype, int ytype, bool res32, cudaStream_t stream, int sms) {
+    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_BF16) return unpermute_residual<__nv_bfloat16, __nv_bfloat16>(a, res32, stream, sms);
+    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP16) return unpermute_residual<__half, __half>(a, res32, stream, sms);
+    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP32) return unpermute_residual<float, float>(a, res32, stream, sms);
+    if (ztype == DPA_DTYPE_BF16 && ytype == DPA_DTYPE_FP32) return unpermute_residual<__nv_bfloat16, float>(a, res32, stream, sms);
+    if (ztype == DPA_DTYPE_FP16 && ytype == DPA_DTYPE_FP32) return unpermute_residual<__half, float>(a, res32, stream, sms);
+    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_BF16) return unpermute_residual<float, __nv_bfloat16>(a, res32, stream, sms);
+    if (ztype == DPA_DTYPE_FP32 && ytype == DPA_DTYPE_FP16) return unpermute_residual<float, __half>(a, res32, stream, sms);
     return cudaErrorInvalidValue;
 }
 

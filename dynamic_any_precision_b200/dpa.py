@@ -51,7 +51,7 @@ class LayerWeights(ctypes.Structure):
 
 class LinearDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
-                ("rows", "in_features", "out_features", "dtype", "out_dtype", "act")]
+                ("rows", "in_features", "out_features", "dtype", "out_dtype", "act", "residual_dtype")]
 
 
 class Aux(ctypes.Structure):
@@ -115,7 +115,7 @@ def lib() -> ctypes.CDLL:
     L.dpa_sort_workspace_size.restype = sz
     L.dpa_sort_pairs.argtypes = [vp, i32, i32, vp, vp, vp, vp, sz, vp]
     L.dpa_permute_rows.argtypes = [i32, vp, vp, i32, i32, i32, vp, vp]
-    L.dpa_unpermute_rows.argtypes = [i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, vp, vp]
+    L.dpa_unpermute_rows.argtypes = [i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]
     L.dpa_unpermute_rows_backward.argtypes = [i32, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
     L.dpa_linear.argtypes = [P(LinearDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.dpa_grouped_linear.argtypes = [P(LinearDesc), i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -514,15 +514,16 @@ def _out(out, shape, like, residual, out_dtype, stream):
 
 def unpermute_rows(z, pos, weights=None, residual=None, out=None, out_dtype=None, stream=None):
     """y[t] = residual[t] + sum_k weights[t][k] * z[pos[t][k]]. z: [T*K][H]; pos: int32 [T][K];
-    weights: fp32 or fp64 [T][K] (None: all 1); residual: [T][H] of y's type, may be `out`. y has
-    out_dtype (default: residual's, else z's): z's own type, or one of the two is fp32."""
+    weights: fp32 or fp64 [T][K] (None: all 1); residual: [T][H] of y's type or fp32, may be `out`.
+    y has out_dtype (default: residual's, else z's): z's own type, or one of the two is fp32."""
     dev, (T, K), H = _device(z), pos.shape, z.shape[-1]
     out = _out(out, (T, H), z, residual, out_dtype, stream)
     code, zcode, wcode = _float_type(out), _float_type(z), _real(weights)
+    rcode = code if residual is None else _float_type(residual)
     _call(lib().dpa_unpermute_rows, "dpa_unpermute_rows", dev, stream, zcode,
           _arg(z, "z", (T * K, H), zcode, dev), _arg(pos, "pos", (T, K), "int32", dev),
           _opt(weights, "weights", (T, K), wcode, dev), wcode,
-          _opt(residual, "residual", (T, H), code, dev), code, T, K, H, _arg(out, "out", (T, H), code, dev))
+          _opt(residual, "residual", (T, H), rcode, dev), rcode, code, T, K, H, _arg(out, "out", (T, H), code, dev))
     return out
 
 
@@ -562,20 +563,21 @@ def _product(x, w, lead, bias, act, w_mul, bias_mul, residual, out, out_dtype, d
     (rows, K), N, code = x.shape, w.shape[-2], _float_type(x)
     out = _out(out, (rows, N), x, residual, out_dtype, stream)
     ocode, wide, flat = _float_type(out), lead + (N, K), lead + (N,)
+    rcode = ocode if residual is None else _float_type(residual)
     if act not in ACTS:
         raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
     ptrs = (_arg(w, "w", wide, code, dev), _opt(bias, "bias", flat, code, dev), _opt(w_mul, "w_mul", wide, code, dev),
-            _opt(bias_mul, "bias_mul", flat, code, dev), _opt(residual, "residual", (rows, N), ocode, dev),
+            _opt(bias_mul, "bias_mul", flat, code, dev), _opt(residual, "residual", (rows, N), rcode, dev),
             _arg(out, "out", (rows, N), ocode, dev))
-    return ctypes.byref(LinearDesc(rows, K, N, code, ocode, ACTS[act])), ptrs, out
+    return ctypes.byref(LinearDesc(rows, K, N, code, ocode, ACTS[act], rcode)), ptrs, out
 
 
 def linear(x, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=None, out=None, out_dtype=None,
            stream=None):
     """out = act(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual]. x: [M][K] bf16 (or int16
-    bits) or fp16, K a multiple of 8; w, w_mul: [N][K]; bias, bias_mul: [N], all of x's type; out and
-    residual: [M][N] in x's type or fp32 (out_dtype; default: residual's, else x's); residual may be
-    `out`. act: "none", "relu", "gelu", "gelu_tanh" or "silu". ws: new_linear_workspace or any
+    bits) or fp16, K a multiple of 8; w, w_mul: [N][K]; bias, bias_mul: [N], all of x's type; out:
+    [M][N] in x's type or fp32 (out_dtype; default: residual's, else x's); residual: [M][N] of
+    out's type or fp32, may be `out`. act: "none", "relu", "gelu", "gelu_tanh" or "silu". ws: new_linear_workspace or any
     other workspace; it receives the device error flag."""
     dev = _device(x)
     desc, ptrs, out = _product(x, w, (), bias, act, w_mul, bias_mul, residual, out, out_dtype, dev, stream)

@@ -464,12 +464,12 @@ dpa_status dpa_permute_rows(int dtype, const void* x, const int32_t* pos, int n_
 /* y[t] = residual[t] + sum_k weights[t][k] * z[pos[t][k]] (device), added in slot order in fp32
  * and rounded once. z [n_tokens*top_k][hidden] of `dtype`; weights [n_tokens][top_k] of
  * weight_dtype (fp32 or fp64; rounded to fp32) or NULL (all 1); residual [n_tokens][hidden] of
- * out_dtype or NULL, may be y itself; y [n_tokens][hidden] of out_dtype. The two types are equal,
- * or one of them is fp32. Pairs with a place outside [0, n_tokens*top_k) add nothing (their row
+ * residual_dtype (out_dtype or fp32) or NULL, may be y itself; y [n_tokens][hidden] of out_dtype.
+ * The types of z and y are equal, or one of them is fp32. Pairs with a place outside [0, n_tokens*top_k) add nothing (their row
  * of z is not read): a token without pairs gets its residual, or 0. */
 dpa_status dpa_unpermute_rows(int dtype, const void* z, const int32_t* pos, const void* weights, int weight_dtype,
-                              const void* residual, int out_dtype, int n_tokens, int top_k, int hidden, void* y,
-                              void* stream);
+                              const void* residual, int residual_dtype, int out_dtype, int n_tokens, int top_k,
+                              int hidden, void* y, void* stream);
 
 /* Gradients of dpa_unpermute_rows (device): dz[pos[t][k]] = weights[t][k] * dy[t] and
  * dweights[t][k] = <dy[t], z[pos[t][k]]> (fp32, 0 for pairs without a place). dy, z, dz of `dtype`;
@@ -482,8 +482,9 @@ dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z,
 /* Matrix product with a fused epilogue (device):
  *     out = act(x W^T + bias) [* (x U^T + bias_mul)] [+ residual]
  * x [rows][in_features], w (and w_mul, U) [out_features][in_features], bias and bias_mul
- * [out_features], all of `dtype` (bf16 or fp16); out and residual [rows][out_features] of
- * out_dtype (`dtype` or fp32); residual may be out itself. bias, w_mul, bias_mul, residual may be
+ * [out_features], all of `dtype` (bf16 or fp16); out [rows][out_features] of out_dtype
+ * (`dtype` or fp32); residual [rows][out_features] of residual_dtype (out_dtype or fp32), may be out
+ * itself. bias, w_mul, bias_mul, residual may be
  * NULL. Products are summed in fp32; out is rounded once. gelu is v*Phi(v), gelu_tanh its tanh
  * form. in_features must be a multiple of 8; any rows and out_features >= 1.
  * ws: device, zero-filled once, at least DPA_LINEAR_WORKSPACE_BYTES (any workspace of this
@@ -491,7 +492,7 @@ dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z,
 #define DPA_LINEAR_WORKSPACE_BYTES 256
 typedef struct dpa_linear_desc {
     int32_t rows, in_features, out_features;
-    int32_t dtype, out_dtype, act;
+    int32_t dtype, out_dtype, act, residual_dtype;   /* residual_dtype: read with a residual only */
 } dpa_linear_desc;
 dpa_status dpa_linear(const dpa_linear_desc* desc, const void* x, const void* w, const void* bias, const void* w_mul,
                       const void* bias_mul, const void* residual, void* out, void* ws, size_t ws_bytes, void* stream);

@@ -42,8 +42,8 @@ def test_row_call_arguments():
     def permute(dtype=0, x=BUF, pos=BUF, T=4, K=2, H=64, out=BUF):
         return L.dpa_permute_rows(dtype, x, pos, T, K, H, out, None)
 
-    def unpermute(dtype=0, z=BUF, pos=BUF, w=BUF, wt=2, res=None, odt=0, T=4, K=2, H=64, y=BUF):
-        return L.dpa_unpermute_rows(dtype, z, pos, w, wt, res, odt, T, K, H, y, None)
+    def unpermute(dtype=0, z=BUF, pos=BUF, w=BUF, wt=2, res=None, rdt=0, odt=0, T=4, K=2, H=64, y=BUF):
+        return L.dpa_unpermute_rows(dtype, z, pos, w, wt, res, rdt, odt, T, K, H, y, None)
 
     def backward(dtype=0, dy=BUF, z=BUF, pos=BUF, w=BUF, wt=2, T=4, K=2, H=64, dz=BUF, dw=BUF):
         return L.dpa_unpermute_rows_backward(dtype, dy, z, pos, w, wt, T, K, H, dz, dw, None)
@@ -56,14 +56,15 @@ def test_row_call_arguments():
         assert f(T=1 << 28, K=8) == 2
     assert permute(x=None) == 1 and permute(x=ODD) == 1 and permute(out=None) == 1 and permute(out=ODD) == 1
     for bad in (dict(z=None), dict(y=None), dict(z=ODD), dict(y=ODD), dict(res=ODD), dict(w=ODD), dict(wt=0),
-                dict(wt=1), dict(odt=1), dict(odt=3), dict(dtype=1, odt=0)):
+                dict(wt=1), dict(odt=1), dict(odt=3), dict(dtype=1, odt=0),
+                dict(res=BUF, rdt=1), dict(res=BUF, rdt=3)):
         assert unpermute(**bad) == 1, bad
     for bad in (dict(dy=None), dict(z=None), dict(w=None), dict(dz=None), dict(dw=None), dict(dy=ODD), dict(dw=ODD),
                 dict(wt=1)):
         assert backward(**bad) == 1, bad
 
 
-def linear(desc=(4, 64, 32, 0, 0, 0), x=BUF, w=BUF, b=None, u=None, c=None, r=None, out=BUF, ws=BUF, n=256, groups=None,
+def linear(desc=(4, 64, 32, 0, 0, 0, 0), x=BUF, w=BUF, b=None, u=None, c=None, r=None, out=BUF, ws=BUF, n=256, groups=None,
            offsets=BUF):
     d = dpa.LinearDesc(*desc)
     if groups is None:
@@ -81,6 +82,7 @@ def test_product_arguments(groups):
                        ((4, 64, 32, 1, 0, 0), 1), ((4, 64, 32, 0, 3, 0), 1), ((4, 64, 32, 0, 0, 5), 1),
                        ((4, 64, 32, 0, 0, -1), 1)):
         assert f(desc=desc) == code, desc
+    assert f(desc=(4, 64, 32, 0, 0, 0, 1), r=BUF) == 1 and f(desc=(4, 64, 32, 0, 2, 0, 0), r=BUF) == 1
     for name in ("x", "w", "out", "ws"):
         assert f(**{name: None}) == 1 and f(**{name: ODD}) == 1, name
     for name in ("b", "u", "r"):

@@ -145,7 +145,7 @@ def test_unpermute_rows(T, K, E, H, drop, types):
     z[live:] = float("nan")     # rows that no pair takes are not read
     for wdt in (torch.float64, torch.float32, None):
         w = None if wdt is None else torch.rand((T, K), generator=g, device="cuda").to(wdt)
-        for res in (None, normal(g, T, H, dtype=yt)):
+        for res in (None, normal(g, T, H, dtype=yt), normal(g, T, H)):
             y = dpa.unpermute_rows(z, pos, w, residual=res, out_dtype=yt)
             terms = torch.where((pos >= 0)[:, :, None], z[pos.clamp_min(0).long()].double(), 0.0)
             if w is not None:
@@ -369,7 +369,10 @@ def test_linear(rows, K, N, act, gated, bias, residual, dtype, out):
     ref, tol = product64(x, w, b, act, u, c, r, DT[out])
     close(y, ref, tol)
     assert torch.equal(dpa.linear(x, w, ws, bias=b, act=act, w_mul=u, bias_mul=c, residual=r, out_dtype=DT[out]), y)
-    if r is not None:   # in place on the residual
+    if r is not None:   # an fp32 residual under any output; in place on the residual
+        r32 = r.float() + 2.0 ** -12
+        ref, tol = product64(x, w, b, act, u, c, r32, DT[out])
+        close(dpa.linear(x, w, ws, bias=b, act=act, w_mul=u, bias_mul=c, residual=r32, out_dtype=DT[out]), ref, tol)
         h = r.clone()
         dpa.linear(x, w, ws, bias=b, act=act, w_mul=u, bias_mul=c, residual=h, out=h)
         assert torch.equal(h, y)
@@ -546,6 +549,8 @@ def test_refusals_on_the_device():
         dpa.linear(x, w, ws, act="tanh")
     with pytest.raises(ValueError):
         dpa.linear(x, w, ws, residual=torch.zeros((4, 9), device="cuda"))
+    with pytest.raises(dpa.DpaError):
+        dpa.linear(x, w, ws, residual=torch.zeros((4, 8), device="cuda").half(), out_dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         dpa.linear(x, w, ws.cpu())
     for bad in (dict(out_dtype=torch.float16), dict(bias_mul=w[:, 0].contiguous())):
