@@ -599,6 +599,77 @@ def grouped_linear(x, offsets, w, ws, bias=None, act="none", w_mul=None, bias_mu
     return out
 
 
+class DenseLayer:
+    """One MoE layer at full precision (bf16 experts, nothing encoded) around the same router: the
+    layer that the bitplane layer's budgets are compared with. Tensors on one device: w_gate, w_up
+    [E][inter][hidden], w_down [E][hidden][inter], w_router [E][hidden], shared None or (gate, up
+    [S][inter][hidden], down [S][hidden][inter]), all bf16 or int16 bits."""
+
+    def __init__(self, desc: LayerDesc, w_gate, w_up, w_down, w_router, shared=None):
+        self.desc = desc
+        self.w_gate, self.w_up, self.w_down, self.w_router, self.shared = w_gate, w_up, w_down, w_router, shared
+
+    @classmethod
+    def from_host(cls, desc: LayerDesc, w_gate: np.ndarray, w_up: np.ndarray, w_down: np.ndarray,
+                  w_router_bits: np.ndarray, shared_bits=None, device="cuda"):
+        """From host fp32 experts (the arrays that encode takes), rounded to bf16 on the device, and
+        bf16 bits of the router and the shared experts."""
+        import torch
+
+        def dev(a):
+            return torch.from_numpy(np.ascontiguousarray(a)).to(device)
+
+        gate, up, down = (dev(w.astype(np.float32, copy=False)).to(torch.bfloat16) for w in (w_gate, w_up, w_down))
+        shared = None if shared_bits is None else tuple(dev(s.view(np.int16)).view(torch.bfloat16) for s in shared_bits)
+        return cls(desc, gate, up, down, dev(w_router_bits.view(np.int16)), shared)
+
+    def buffers(self, n_tokens: int):
+        """Workspaces and intermediate rows of dense_moe_forward for n_tokens tokens."""
+        import torch
+        d, dev = self.desc, self.w_gate.device
+        P = n_tokens * d.top_k
+
+        def new(*shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        bufs = {"ws": new_workspace(d, n_tokens, device=dev), "sort_ws": new_sort_workspace(P, d.n_experts, device=dev),
+                "pos": new(n_tokens, d.top_k, dtype=torch.int32), "order": new(P, dtype=torch.int32),
+                "offsets": new(d.n_experts + 1, dtype=torch.int32), "rows": new(P, d.hidden, dtype=torch.bfloat16),
+                "h": new(P, d.inter, dtype=torch.bfloat16), "z": new(P, d.hidden, dtype=torch.float32)}
+        if self.shared is not None:
+            bufs["shared_h"] = new(n_tokens, d.inter, dtype=torch.bfloat16)
+            bufs["shared_y"] = new(n_tokens, d.hidden, dtype=torch.float32)
+        return bufs
+
+
+def dense_moe_forward(layer: DenseLayer, x, bufs, y=None, aux: Optional[dict] = None, stream=None):
+    """One MoE layer at full precision: route, sort the pairs by expert, the experts' gate/up with
+    SwiGLU and down products on each expert's rows, and the gate-weighted sum back to the tokens, on
+    top of the shared experts' outputs. x: CUDA int16/bf16 bits [T][H]; bufs: layer.buffers(T). aux:
+    optional dict that receives "topk_idx" and "topk_gate". The SwiGLU output is rounded to bf16
+    between the two products, every other intermediate is fp32. Returns y (int16 bf16 bits [T][H])."""
+    import torch
+    ws = bufs["ws"]
+    if y is None:
+        y = _new(x, x.shape, torch.int16, stream)
+    idx, gate = route(layer.desc, x, layer.w_router, ws, stream=stream)
+    if aux is not None:
+        aux["topk_idx"], aux["topk_gate"] = idx, gate
+    xb = x.view(torch.bfloat16)
+    acc = None
+    for s in range(0 if layer.shared is None else layer.desc.n_shared):
+        g, u, d = (m[s] for m in layer.shared)
+        linear(xb, g, ws, act="silu", w_mul=u, out=bufs["shared_h"], stream=stream)
+        acc = linear(bufs["shared_h"], d, ws, residual=acc, out=bufs["shared_y"], stream=stream)
+    sort_pairs(idx, layer.desc.n_experts, bufs["sort_ws"], bufs["pos"], bufs["order"], bufs["offsets"], stream=stream)
+    permute_rows(xb, bufs["pos"], out=bufs["rows"], stream=stream)
+    grouped_linear(bufs["rows"], bufs["offsets"], layer.w_gate, ws, act="silu", w_mul=layer.w_up, out=bufs["h"],
+                   stream=stream)
+    grouped_linear(bufs["h"], bufs["offsets"], layer.w_down, ws, out=bufs["z"], stream=stream)
+    unpermute_rows(bufs["z"], bufs["pos"], gate, residual=acc, out=y, stream=stream)
+    return y
+
+
 def stream_prefixes(desc: LayerDesc, host_planes, host_meta, experts, kplanes, dev_planes, dev_meta,
                     stream=None) -> int:
     """Copy the first kplanes[i] planes (and their scale data) of experts[i] from the host
