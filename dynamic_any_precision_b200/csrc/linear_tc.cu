@@ -15,9 +15,9 @@
 //           its 128 weight rows and half of the tokens, so a 64-wide K step moves 32 KB per SM for
 //           512 cycles of MMA. For compute-bound sizes; persistent, one pair per two SMs.
 //   CG = 1  one CTA per tile of 128 weight rows x up to 128 tokens. For weight-bound sizes. With
-//           few tiles, a cluster of S CTAs splits K: every CTA leaves its partial sums in shared
-//           memory, and each then adds up its share of the outputs over the cluster, in rank
-//           order (deterministic), before the epilogue.
+//           few tiles, a cluster of S CTAs splits K: every CTA sends its partial sums of token u
+//           into the shared memory of CTA u mod S, which adds them up in rank order
+//           (deterministic) before the epilogue.
 //
 // Roles (576 threads): warps 0-15 epilogue (four per TMEM lane quadrant; with eight, an epilogue of
 // 256 tokens took longer than 2048 inputs' MMAs), warp 16 TMA loads (no multicast), warp 17 TMEM
@@ -76,22 +76,23 @@ __device__ __forceinline__ int group_edge(const LinearArgs& a, int e) {
 template <int CG>
 __device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref, int tile) {
     Tile t;
-    int tt = tile / a.FT;
+    int tt = static_cast<int>(static_cast<unsigned>(tile) / static_cast<unsigned>(a.FT));
     t.ft = tile - tt * a.FT;
     t.e = 0;
-    int begin = 0, n = a.rows;
-    if (a.E > 0) {   // the last group whose first token tile is not after tt
-        int lo = 0, hi = a.E - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_pref[mid] <= tt) lo = mid;
-            else hi = mid - 1;
-        }
-        t.e = lo;
-        tt -= s_pref[lo];
-        begin = group_edge(a, lo);
-        n = group_edge(a, lo + 1) - begin;
+    if (a.E == 0) {   // plain: the launcher's TN is the tiles' size
+        t.row0 = tt * a.TN;
+        t.n = min(a.rows - t.row0, a.TN);
+        return t;
     }
+    int lo = 0, hi = a.E - 1;   // the last group whose first token tile is not after tt
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_pref[mid] <= tt) lo = mid;
+        else hi = mid - 1;
+    }
+    t.e = lo;
+    tt -= s_pref[lo];
+    const int begin = group_edge(a, lo), n = group_edge(a, lo + 1) - begin;
     const int sz = balanced_rows(n, a.TN, 16 * CG);
     t.row0 = begin + tt * sz;
     t.n = min(n - tt * sz, sz);
@@ -253,13 +254,64 @@ __device__ __forceinline__ void load3d(uint32_t dst, const CUtensorMap* map, int
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// Eight biases of one group's features (zeros without a bias and behind the last feature).
+template <bool F16>
+__device__ __forceinline__ void load_bias(const void* b, int64_t at, bool vec, int cnt, Two (&out)[4]) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (b && cnt > 0) {
+        const uint16_t* p = static_cast<const uint16_t*>(b) + at;
+        if (vec) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = v.x;
+            w[1] = v.y;
+            w[2] = v.z;
+            w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = (2 * i < cnt ? __ldg(p + 2 * i) : 0u) |
+                       (2 * i + 1 < cnt ? static_cast<uint32_t>(__ldg(p + 2 * i + 1)) << 16 : 0u);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = two(up16<F16>(static_cast<uint16_t>(w[i])), up16<F16>(static_cast<uint16_t>(w[i] >> 16)));
+}
+
+// Bias, activation and gate of eight sums (g; m: the second product's).
+template <bool GATED>
+__device__ __forceinline__ void finish8(Two (&g)[4], const Two (&m)[4], const Two (&bias)[4], const Two (&bmul)[4], int act,
+                                        float (&o)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) g[e] = add2(g[e], bias[e]);
+    act_many(g, act);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (GATED) g[e] = mul2(g[e], add2(m[e], bmul[e]));
+        const float2 h = apart(g[e]);
+        o[2 * e] = h.x;
+        o[2 * e + 1] = h.y;
+    }
+}
+__device__ __forceinline__ void load_sums(const float* p0, const float* p1, Two (&v)[4]) {
+    const float4 x = *reinterpret_cast<const float4*>(p0), y = *reinterpret_cast<const float4*>(p1);
+    v[0] = two(x.x, x.y);
+    v[1] = two(x.z, x.w);
+    v[2] = two(y.x, y.y);
+    v[3] = two(y.z, y.w);
 }
 
 template <int CG, bool GATED, bool F16>
@@ -273,8 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     const int stages = a.stages, btile = (a.TN / CG) * 128;
     unsigned char* sA = sm;
     unsigned char* sB = sm + stages * kATile;
-    float* s_out = reinterpret_cast<float*>(sB + stages * btile);   // [kGroups][kChunk][128] epilogue staging
-    unsigned char* tail = sB + stages * btile + kOutBytes;
+    // epilogue staging [kGroups][kChunk][128]; K split: [splits][this CTA's tokens][128] partial sums
+    float* s_out = reinterpret_cast<float*>(sB + stages * btile);
+    unsigned char* tail = sB + stages * btile + a.out_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(tail);
     uint64_t* empty = full + kMaxStages;
     uint64_t* acc_full = empty + kMaxStages;
@@ -303,6 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         *s_abort = 0;
         fence_barrier_init();
     }
+    if (warp == kLoadWarp && lane == 0) {
+        prefetch_map(&wmap);
+        if (GATED) prefetch_map(&umap);
+        prefetch_map(&xmaps.m[0]);
+    }
+    if (CG == 1 && S > 1) cluster_arrive();   // waited for before the first access to another CTA's memory
     if (warp == kMmaWarp) {
         if constexpr (CG == 1) {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -347,12 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     if constexpr (CG == 2) cluster_sync();   // the pair's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const int ttiles = a.E > 0 ? s_pref[a.E] : (a.rows + a.TN - 1) / a.TN;
-    int64_t ntiles = static_cast<int64_t>(ttiles) * a.FT;
+    int ntiles = a.E > 0 ? s_pref[a.E] * a.FT : a.ntiles;
     if (S > 1 && ntiles > ncl) ntiles = ncl;   // one tile per cluster (only offsets out of order name more)
     // this CTA's K steps
-    const int k0 = CG == 1 ? static_cast<int>(static_cast<int64_t>(a.ksteps) * rank / S) : 0;
-    const int k1 = CG == 1 ? static_cast<int>(static_cast<int64_t>(a.ksteps) * (rank + 1) / S) : a.ksteps;
+    const int k0 = CG == 1 ? a.ksteps * rank / S : 0, k1 = CG == 1 ? a.ksteps * (rank + 1) / S : a.ksteps;
 
     if (warp == kLoadWarp) {
         // ================= loads =================
@@ -364,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
             int s = 0, ph = 1;
             bool ok = true;
-            for (int64_t it = cid; it < ntiles && ok; it += ncl) {
-                const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
+            for (int it = cid; it < ntiles && ok; it += ncl) {
+                const Tile t = find_tile<CG>(a, s_pref, it);
                 const int part = ((t.n + 16 * CG - 1) / (16 * CG)) * 16;   // token rows of this CTA
                 int mi = 0, box = a.xbox;
                 while (box < part) {   // grouped only: a plain tile's box holds it
@@ -409,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             const uint64_t dconst = smem_desc_sw128(0);
             int s = 0, ph = 0, j = 0;
             bool ok = true;
-            for (int64_t it = cid; it < ntiles && ok; it += ncl, ++j) {
-                const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
+            for (int it = cid; it < ntiles && ok; it += ncl, ++j) {
+                const Tile t = find_tile<CG>(a, s_pref, it);
                 const int b = j & 1;
                 const int ncols = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
                 const uint32_t idesc = instr_desc(F16 ? 0 : 1, ncols, 128 * CG);
@@ -473,9 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             empty_bar[1] = mapa_shared(empty_bar[1], 0);
         }
         const bool vec = (a.N & 7) == 0;
+        if (CG == 1 && S > 1) cluster_wait();   // every CTA of the cluster has started
         int j = 0;
-        for (int64_t it = cid; it < ntiles; it += ncl, ++j) {
-            const Tile t = find_tile<CG>(a, s_pref, static_cast<int>(it));
+        for (int it = cid; it < ntiles; it += ncl, ++j) {
+            const Tile t = find_tile<CG>(a, s_pref, it);
             const int b = j & 1;
             const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + fg * 8;
             const int cnt = min(max(a.N - f, 0), 8);
@@ -484,14 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             Out8 res[kItems];
             if (CG == 2 || S == 1) {   // operands of the epilogue: loaded while the MMAs run
                 const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in0 = 2 * i < cnt, in1 = 2 * i + 1 < cnt;
-                    bias[i] = two(in0 ? bias_at<F16>(a.bias, fb + 2 * i) : 0.f, in1 ? bias_at<F16>(a.bias, fb + 2 * i + 1) : 0.f);
-                    if (GATED)
-                        bmul[i] = two(in0 ? bias_at<F16>(a.bias_mul, fb + 2 * i) : 0.f,
-                                      in1 ? bias_at<F16>(a.bias_mul, fb + 2 * i + 1) : 0.f);
-                }
+                load_bias<F16>(a.bias, fb, vec, cnt, bias);
+                if (GATED) load_bias<F16>(a.bias_mul, fb, vec, cnt, bmul);
                 if (a.residual && cnt > 0) {
 #pragma unroll
                     for (int i = 0; i < kItems; ++i) {
@@ -507,15 +559,23 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             tc_fence_after();
             const uint32_t acc = tmem + lane_base + static_cast<uint32_t>(b) * kAccCols;
             if (CG == 1 && S > 1) {
-                // partial sums [token][128] into the (now idle) stage memory
-                float* part = reinterpret_cast<float*>(sm);
+                // token u goes to CTA u mod S of the cluster: [this CTA's rank][u / S][128]
+                const int slice = (t.n + S - 1) / S * kRowsA;
+                const uint32_t dst = smem_u32(s_out) + static_cast<uint32_t>(rank * slice + R) * 4;
                 for (int c = grp; c < nch; c += kGroups) {
                     uint32_t v[kChunk];
                     tmem_ld16(acc + kChunk * c, v);
+                    int place = kChunk * c / S, owner = kChunk * c - place * S;
                     tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < kChunk; ++u)
-                        if (kChunk * c + u < t.n) part[(kChunk * c + u) * kRowsA + R] = __uint_as_float(v[u]);
+                    for (int u = 0; u < kChunk; ++u) {
+                        if (kChunk * c + u < t.n)
+                            st_cluster_f32(mapa_shared(dst + static_cast<uint32_t>(place * kRowsA) * 4, owner), __uint_as_float(v[u]));
+                        if (++owner == S) {
+                            owner = 0;
+                            ++place;
+                        }
+                    }
                 }
                 break;   // one tile per cluster
             }
@@ -541,26 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                         const int in = tk0 + i * kTokStep, tok = kChunk * c + in;
                         if (tok >= t.n) break;
                         const int64_t at = (static_cast<int64_t>(t.row0) + tok) * a.N + f;
-                        const float4 x0 = *reinterpret_cast<const float4*>(get0 + in * kRowsA);
-                        const float4 x1 = *reinterpret_cast<const float4*>(get1 + in * kRowsA);
-                        Two g2[4] = {two(x0.x, x0.y), two(x0.z, x0.w), two(x1.x, x1.y), two(x1.z, x1.w)};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) g2[e] = add2(g2[e], bias[e]);
-                        act_many(g2, a.act);
-                        if constexpr (GATED) {
-                            const float4 m0 = *reinterpret_cast<const float4*>(gum0 + in * kRowsA);
-                            const float4 m1 = *reinterpret_cast<const float4*>(gum1 + in * kRowsA);
-                            const Two m[4] = {two(m0.x, m0.y), two(m0.z, m0.w), two(m1.x, m1.y), two(m1.z, m1.w)};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) g2[e] = mul2(g2[e], add2(m[e], bmul[e]));
-                        }
+                        Two g2[4], m2[4];
+                        load_sums(get0 + in * kRowsA, get1 + in * kRowsA, g2);
+                        if (GATED) load_sums(gum0 + in * kRowsA, gum1 + in * kRowsA, m2);
                         float g[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 h = apart(g2[e]);
-                            g[2 * e] = h.x;
-                            g[2 * e + 1] = h.y;
-                        }
+                        finish8<GATED>(g2, m2, bias, bmul, a.act, g);
                         if (a.residual) {
                             add_residual<F16>(a, res[i], g);
                             if (tok + kChunk * kGroups < t.n)
@@ -582,40 +627,45 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     __syncwarp();
 
     if (CG == 1 && S > 1) {
-        cluster_sync();   // every CTA's partial sums are written
+        if (warp >= kEpiWarps) cluster_wait();   // the first phase, which the epilogue has waited for
+        __syncwarp();
+        cluster_sync();                          // every partial sum has arrived
         if (cid < ntiles) {
             const Tile t = find_tile<CG>(a, s_pref, cid);
-            const int f0 = t.ft * kFeat, tot = t.n * kFeat;
-            const int i1 = static_cast<int>(static_cast<int64_t>(tot) * (rank + 1) / S);
-            const uint32_t base = smem_u32(sm);
-            uint32_t peer[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) peer[r] = mapa_shared(base, r < S ? r : 0);
-            for (int i = static_cast<int>(static_cast<int64_t>(tot) * rank / S) + tid; i < i1; i += kThreads) {
-                const int tok = i / kFeat, fi = i - tok * kFeat, f = f0 + fi;
-                if (f >= a.N) continue;
-                const uint32_t off =
-                    static_cast<uint32_t>(tok * kRowsA + fi) * 4;
-                float pv[8], pm[8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    pv[r] = r < S ? ld_cluster_f32(peer[r] + off) : 0.f;
-                    pm[r] = GATED && r < S ? ld_cluster_f32(peer[r] + off + 64 * 4) : 0.f;
-                }
-                float v = pv[0], m = pm[0];
-#pragma unroll
-                for (int r = 1; r < 8; ++r) {
-                    v += pv[r];
-                    m += pm[r];
-                }
+            const int slice = (t.n + S - 1) / S * kRowsA, mine = (t.n - rank + S - 1) / S;
+            const bool vec = (a.N & 7) == 0;
+            for (int i = tid; i < mine * (kFeat / 8); i += kThreads) {
+                const int place = i / (kFeat / 8), fg = i % (kFeat / 8), f = t.ft * kFeat + fg * 8;
+                const int cnt = min(max(a.N - f, 0), 8);
+                if (cnt == 0) continue;
                 const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
-                float o = act_one(v + bias_at<F16>(a.bias, fb), a.act);
-                if (GATED) o *= m + bias_at<F16>(a.bias_mul, fb);
-                const int64_t at = (static_cast<int64_t>(t.row0) + tok) * a.N + f;
-                store_one<F16>(a, o, at);
+                const int64_t at = (static_cast<int64_t>(t.row0) + place * S + rank) * a.N + f;
+                Two bias[4], bmul[4], g[4], m[4];
+                Out8 res;
+                load_bias<F16>(a.bias, fb, vec, cnt, bias);
+                if (GATED) load_bias<F16>(a.bias_mul, fb, vec, cnt, bmul);
+                if (a.residual) res = load_residual(a, at, vec, cnt);
+                const float* src = s_out + place * kRowsA + fg * 8;
+                load_sums(src, src + 4, g);
+                if (GATED) load_sums(src + 64, src + 68, m);
+                for (int r = 1; r < S; ++r) {   // in rank order
+                    Two x[4];
+                    src += slice;
+                    load_sums(src, src + 4, x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) g[e] = add2(g[e], x[e]);
+                    if (GATED) {
+                        load_sums(src + 64, src + 68, x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[e] = add2(m[e], x[e]);
+                    }
+                }
+                float o[8];
+                finish8<GATED>(g, m, bias, bmul, a.act, o);
+                if (a.residual) add_residual<F16>(a, res, o);
+                store_out<F16>(a, o, at, vec, cnt);
             }
         }
-        cluster_sync();   // no CTA leaves while another reads its partial sums
     }
     tc_fence_before();
     __syncthreads();
@@ -702,11 +752,14 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
         a.xbox = a.TN / CG;
         const int64_t tiles = static_cast<int64_t>((a.rows - 1) / a.TN + 1) * a.FT;
         if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+        a.ntiles = static_cast<int>(tiles);
         if (!pair)
             while (a.splits < 8 && a.splits < a.ksteps && tiles * (a.splits + 1) <= sms) ++a.splits;
         clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
     }
-    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + kOutBytes + kBarBytes + (a.E + 1) * 4;
+    a.out_bytes = kOutBytes;
+    if (a.splits > 1 && (a.TN + a.splits) * kRowsA * 4 > kOutBytes) a.out_bytes = (a.TN + a.splits) * kRowsA * 4;
+    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + a.out_bytes + kBarBytes + (a.E + 1) * 4;
     a.stages = (kSmemMax - fixed) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const size_t smem = static_cast<size_t>(a.stages) * stage + fixed;
