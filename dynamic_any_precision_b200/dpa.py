@@ -366,61 +366,51 @@ def residual_rmsnorm(h, x, y=None, stream=None):
 
 # ------------------------------------------------------------- dense experts: rows and products
 
-_DTYPES = None
-_current_device = _raw_stream = None
+_DTYPES = _FLOATS = None
+_current_device = _raw_stream = _empty_like = None
 
 
 def _torch_tables():
-    """Element types and the current device and stream, looked up once (torch is imported late)."""
-    global _DTYPES, _current_device, _raw_stream
+    """Element types and the current device and stream, looked up once (torch is imported late).
+    int16 and uint16 tensors hold bf16 bit patterns."""
+    global _DTYPES, _FLOATS, _current_device, _raw_stream, _empty_like
     import torch
-    _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.uint16: DTYPE_BF16,
-               torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32, torch.float64: DTYPE_FP64,
-               torch.int32: "int32", torch.uint8: "uint8"}
+    _FLOATS = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.uint16: DTYPE_BF16,
+               torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32, torch.float64: DTYPE_FP64}
+    _DTYPES = {**_FLOATS, torch.int32: "int32", torch.uint8: "uint8"}
     _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _empty_like = torch.empty_like
 
 
-def _dtype(t):
-    """DTYPE_* of a tensor's elements (int16 and uint16 tensors hold bf16 bit patterns), or "int32"
-    or "uint8"."""
-    code = _DTYPES.get(t.dtype)
+def _device(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    if _DTYPES is None:
+        _torch_tables()
+    return dev
+
+
+def _float_type(t) -> int:
+    """DTYPE_* of a tensor of floating-point values."""
+    code = _FLOATS.get(t.dtype)
     if code is None:
         raise ValueError(f"unsupported element type {t.dtype}")
     return code
 
 
-def _float_type(t) -> int:
-    """_dtype of a tensor that has to hold floating-point rows."""
-    code = _dtype(t)
-    if not isinstance(code, int):
-        raise ValueError(f"unsupported element type {t.dtype}")
-    return code
-
-
 def _arg(t, name: str, shape, code, dev: int) -> int:
-    """Pointer of a tensor argument, after checking its shape, element type (a code of _dtype),
-    device index and layout."""
+    """Pointer of a tensor argument, after checking its shape, element type (DTYPE_*, "int32" or
+    "uint8"), device index and layout."""
     if t.shape == shape and _DTYPES.get(t.dtype) == code and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if _dtype(t) != code:
+    if _DTYPES.get(t.dtype) != code:
         raise ValueError(f"{name}: unexpected element type {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on cuda:{dev}, got {t.device}")
     raise ValueError(f"{name}: expected a contiguous tensor")
-
-
-def _opt(t, name: str, shape, code, dev: int):
-    return None if t is None else _arg(t, name, shape, code, dev)
-
-
-def _device(t) -> int:
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if _DTYPES is None:
-        _torch_tables()
-    return t.get_device()
 
 
 def _call(fn, where: str, dev: int, stream, *args):
@@ -443,6 +433,15 @@ def _new(like, shape, dtype, stream):
     import torch
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
+
+
+def _like(t, stream):
+    """_new of t's own shape and type."""
+    if stream is None:
+        return _empty_like(t)
+    import torch
+    with torch.cuda.stream(stream):
+        return _empty_like(t)
 
 
 def sort_workspace_size(n_pairs: int, n_experts: int) -> int:
@@ -473,11 +472,11 @@ def sort_pairs(idx, n_experts: int, ws, pos=None, order=None, offsets=None, stre
     (unrouted ones last), the places before each expert."""
     dev, P = _device(idx), idx.numel()
     if pos is None:
-        pos = _new(idx, idx.shape, idx.dtype, stream)
+        pos = _like(idx, stream)
     if order is None:
-        order = _new(idx, (P,), idx.dtype, stream)
+        order = _new(idx, P, idx.dtype, stream)
     if offsets is None:
-        offsets = _new(idx, (n_experts + 1,), idx.dtype, stream)
+        offsets = _new(idx, n_experts + 1, idx.dtype, stream)
     _call(lib().dpa_sort_pairs, "dpa_sort_pairs", dev, stream, _arg(idx, "idx", idx.shape, "int32", dev), P, n_experts,
           _arg(pos, "pos", idx.shape, "int32", dev), _arg(order, "order", (P,), "int32", dev),
           _arg(offsets, "offsets", (n_experts + 1,), "int32", dev), _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
@@ -492,7 +491,7 @@ def permute_rows(x, pos, out=None, stream=None):
     (T, H), K = x.shape, pos.shape[-1]
     if out is None:
         out = _new(x, (T * K, H), x.dtype, stream)
-    _call(lib().dpa_permute_rows, "dpa_permute_rows", dev, stream, code, _arg(x, "x", x.shape, _dtype(x), dev),
+    _call(lib().dpa_permute_rows, "dpa_permute_rows", dev, stream, code, _arg(x, "x", x.shape, code, dev),
           _arg(pos, "pos", (T, K), "int32", dev), T, K, H, _arg(out, "out", (T * K, H), code, dev))
     return out
 
@@ -506,6 +505,8 @@ def _out(out, shape, like, residual, out_dtype, stream):
     """The output tensor of a call: the given one, or a new one of out_dtype (default: the
     residual's type, else `like`'s)."""
     if out is None:
+        if residual is not None and residual.shape == shape and out_dtype in (None, residual.dtype):
+            return _like(residual, stream)
         return _new(like, shape, out_dtype or (like if residual is None else residual).dtype, stream)
     if out_dtype is not None and out.dtype != out_dtype:
         raise ValueError(f"out: unexpected element type {out.dtype}")
@@ -522,8 +523,9 @@ def unpermute_rows(z, pos, weights=None, residual=None, out=None, out_dtype=None
     rcode = code if residual is None else _float_type(residual)
     _call(lib().dpa_unpermute_rows, "dpa_unpermute_rows", dev, stream, zcode,
           _arg(z, "z", (T * K, H), zcode, dev), _arg(pos, "pos", (T, K), "int32", dev),
-          _opt(weights, "weights", (T, K), wcode, dev), wcode,
-          _opt(residual, "residual", (T, H), rcode, dev), rcode, code, T, K, H, _arg(out, "out", (T, H), code, dev))
+          None if weights is None else _arg(weights, "weights", (T, K), wcode, dev), wcode,
+          None if residual is None else _arg(residual, "residual", (T, H), rcode, dev), rcode, code, T, K, H,
+          _arg(out, "out", (T, H), code, dev))
     return out
 
 
@@ -531,7 +533,7 @@ def _real(weights) -> int:
     """DTYPE_* of gate weights (fp32 or fp64), -1 without weights."""
     if weights is None:
         return -1
-    code = _dtype(weights)
+    code = _FLOATS.get(weights.dtype)
     if code not in (DTYPE_FP32, DTYPE_FP64):
         raise ValueError(f"weights: expected fp32 or fp64, got {weights.dtype}")
     return code
@@ -546,7 +548,7 @@ def unpermute_rows_backward(dy, z, pos, weights, dz=None, dweights=None, stream=
     if weights is None:
         raise ValueError("weights: expected a tensor")
     if dz is None:
-        dz = _new(z, z.shape, z.dtype, stream)
+        dz = _like(z, stream)
     if dweights is None:
         import torch
         dweights = _new(z, (T, K), torch.float32, stream)
@@ -557,19 +559,28 @@ def unpermute_rows_backward(dy, z, pos, weights, dz=None, dweights=None, stream=
     return dz, dweights
 
 
-def _product(x, w, lead, bias, act, w_mul, bias_mul, residual, out, out_dtype, dev, stream):
-    """Arguments of linear and grouped_linear (`lead` is () or (n_groups,)): the descriptor, the
-    pointers of w, bias, w_mul, bias_mul, residual and out, and out."""
-    (rows, K), N, code = x.shape, w.shape[-2], _float_type(x)
+def _product(fn, where, x, w, lead, groups, ws, bias, act, w_mul, bias_mul, residual, out, out_dtype, stream):
+    """linear and grouped_linear: `lead` is () or (n_groups,), `groups` the group arguments of the
+    call: () or (n_groups, offsets)."""
+    dev, (rows, K), N = _device(x), x.shape, w.shape[-2]
     out = _out(out, (rows, N), x, residual, out_dtype, stream)
-    ocode, wide, flat = _float_type(out), lead + (N, K), lead + (N,)
+    code, ocode = _float_type(x), _float_type(out)
     rcode = ocode if residual is None else _float_type(residual)
+    wide, flat, rect = lead + (N, K), lead + (N,), (rows, N)
     if act not in ACTS:
         raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
-    ptrs = (_arg(w, "w", wide, code, dev), _opt(bias, "bias", flat, code, dev), _opt(w_mul, "w_mul", wide, code, dev),
-            _opt(bias_mul, "bias_mul", flat, code, dev), _opt(residual, "residual", (rows, N), rcode, dev),
-            _arg(out, "out", (rows, N), ocode, dev))
-    return ctypes.byref(LinearDesc(rows, K, N, code, ocode, ACTS[act], rcode)), ptrs, out
+    xp = _arg(x, "x", x.shape, code, dev)
+    if groups:
+        groups = (groups[0], xp, _arg(groups[1], "offsets", (groups[0] + 1,), "int32", dev))
+    else:
+        groups = (xp,)
+    _call(fn, where, dev, stream, LinearDesc(rows, K, N, code, ocode, ACTS[act], rcode), *groups,
+          _arg(w, "w", wide, code, dev), None if bias is None else _arg(bias, "bias", flat, code, dev),
+          None if w_mul is None else _arg(w_mul, "w_mul", wide, code, dev),
+          None if bias_mul is None else _arg(bias_mul, "bias_mul", flat, code, dev),
+          None if residual is None else _arg(residual, "residual", rect, rcode, dev),
+          _arg(out, "out", rect, ocode, dev), _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
+    return out
 
 
 def linear(x, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=None, out=None, out_dtype=None,
@@ -579,11 +590,8 @@ def linear(x, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=
     [M][N] in x's type or fp32 (out_dtype; default: residual's, else x's); residual: [M][N] of
     out's type or fp32, may be `out`. act: "none", "relu", "gelu", "gelu_tanh" or "silu". ws: new_linear_workspace or any
     other workspace; it receives the device error flag."""
-    dev = _device(x)
-    desc, ptrs, out = _product(x, w, (), bias, act, w_mul, bias_mul, residual, out, out_dtype, dev, stream)
-    _call(lib().dpa_linear, "dpa_linear", dev, stream, desc, _arg(x, "x", x.shape, _dtype(x), dev), *ptrs,
-          _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
-    return out
+    return _product(lib().dpa_linear, "dpa_linear", x, w, (), (), ws, bias, act, w_mul, bias_mul, residual, out,
+                    out_dtype, stream)
 
 
 def grouped_linear(x, offsets, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=None, out=None,
@@ -592,11 +600,9 @@ def grouped_linear(x, offsets, w, ws, bias=None, act="none", w_mul=None, bias_mu
     take w[e]. offsets: int32 [E + 1] on the device (sort_pairs); w, w_mul: [E][N][K]; bias,
     bias_mul: [E][N]. Rows behind offsets[E] are neither used nor written (with out=None:
     uninitialised)."""
-    dev, E = _device(x), w.shape[0]
-    desc, ptrs, out = _product(x, w, (E,), bias, act, w_mul, bias_mul, residual, out, out_dtype, dev, stream)
-    _call(lib().dpa_grouped_linear, "dpa_grouped_linear", dev, stream, desc, E, _arg(x, "x", x.shape, _dtype(x), dev),
-          _arg(offsets, "offsets", (E + 1,), "int32", dev), *ptrs, _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
-    return out
+    E = w.shape[0]
+    return _product(lib().dpa_grouped_linear, "dpa_grouped_linear", x, w, (E,), (E, offsets), ws, bias, act, w_mul,
+                    bias_mul, residual, out, out_dtype, stream)
 
 
 class DenseLayer:
