@@ -15,13 +15,15 @@ bool given16(const void* p) { return p && aligned16(p); }   // required, aligned
 bool opt16(const void* p) { return !p || aligned16(p); }    // optional, aligned
 
 constexpr int64_t kMaxPairs = 1 << 30;
+constexpr int kMaxRowLength = 1 << 24;   // row calls: 32-bit positions inside a row
+constexpr int kMaxInputs = 1 << 22;      // products: a tile's K loop stays far below the kernels' time limit
 
 bool row_type(int t) { return t == DPA_DTYPE_BF16 || t == DPA_DTYPE_FP16 || t == DPA_DTYPE_FP32; }
 
 // tokens, slots and row length of the row calls
 dpa_status check_rows(int T, int K, int H) {
     if (T <= 0 || K <= 0 || H <= 0) return DPA_ERR_INVALID_ARG;
-    if (K > 32 || static_cast<int64_t>(T) * K > kMaxPairs) return DPA_ERR_UNSUPPORTED;
+    if (K > 32 || H > kMaxRowLength || static_cast<int64_t>(T) * K > kMaxPairs) return DPA_ERR_UNSUPPORTED;
     return DPA_OK;
 }
 
@@ -49,7 +51,7 @@ dpa_status run_linear(const dpa_linear_desc* d, int groups, const void* x, const
     if (!given16(x) || !given16(w) || !given16(out) || !given16(ws)) return DPA_ERR_INVALID_ARG;
     if (!opt16(bias) || !opt16(w_mul) || !opt16(bias_mul) || !opt16(residual)) return DPA_ERR_INVALID_ARG;
     if (bias_mul && !w_mul) return DPA_ERR_INVALID_ARG;
-    if (d->in_features % 8) return DPA_ERR_UNSUPPORTED;   // rows of whole 16-byte pieces (tensor loads)
+    if (d->in_features % 8 || d->in_features > kMaxInputs) return DPA_ERR_UNSUPPORTED;   // rows of whole 16-byte pieces (tensor loads)
     if (ws_bytes < DPA_LINEAR_WORKSPACE_BYTES) return DPA_ERR_WORKSPACE;
     dpa::LinearArgs a{};
     a.rows = d->rows;

@@ -277,8 +277,9 @@ struct LinearArgs {
     int act, out32, res32;    // DPA_ACT_*; 1: fp32 output, fp32 residual
     WsHeader* hdr;
     // set by the launcher: K steps, feature tiles, most tokens per tile, CTAs sharing K, pipeline
-    // stages, rows of the smallest token load, tiles (plain), bytes of the epilogue's shared memory
-    int ksteps, FT, TN, splits, stages, xbox, ntiles, out_bytes;
+    // stages, rows of the smallest token load, tiles (plain), bytes of the epilogue's shared memory,
+    // whether out is 32-byte aligned
+    int ksteps, FT, TN, splits, stages, xbox, ntiles, out_bytes, out_wide;
 };
 cudaError_t launch_linear(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
                           cudaStream_t stream, int sms);

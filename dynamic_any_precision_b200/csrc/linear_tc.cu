@@ -152,10 +152,13 @@ template <bool F16>
 __device__ __forceinline__ void store_out(const LinearArgs& a, const float (&v)[8], int64_t at, bool vec, int cnt) {
     if (a.out32) {
         float* p = static_cast<float*>(a.out) + at;
-        if (vec) {   // one 32-byte store
+        if (vec && a.out_wide) {   // one 32-byte store
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
                          "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                          : "memory");
+        } else if (vec) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -796,6 +799,7 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
         if (!pair) a.splits = split_k(tiles, a.ksteps);
         clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
     }
+    a.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // buffers are 16-byte aligned at least
     a.out_bytes = kOutBytes;
     if (a.splits > 1 && (a.TN + a.splits) * kRowsA * 4 > kOutBytes) a.out_bytes = (a.TN + a.splits) * kRowsA * 4;
     const int stage = kATile + a.TN / CG * 128, fixed = 1024 + a.out_bytes + kBarBytes + (a.E + 1) * 4;

@@ -655,24 +655,27 @@ def dense_moe_forward(layer: DenseLayer, x, bufs, y=None, aux: Optional[dict] = 
     optional dict that receives "topk_idx" and "topk_gate". The SwiGLU output is rounded to bf16
     between the two products, every other intermediate is fp32. Returns y (int16 bf16 bits [T][H])."""
     import torch
+    if stream is not None or x.get_device() != torch.cuda.current_device():
+        # every buffer of the call, the router's outputs among them, belongs to the call's stream
+        with torch.cuda.device(_device(x)), torch.cuda.stream(stream):
+            return dense_moe_forward(layer, x, bufs, y, aux)
     ws = bufs["ws"]
     if y is None:
-        y = _new(x, x.shape, torch.int16, stream)
-    idx, gate = route(layer.desc, x, layer.w_router, ws, stream=stream)
+        y = _new(x, x.shape, torch.int16, None)
+    idx, gate = route(layer.desc, x, layer.w_router, ws)
     if aux is not None:
         aux["topk_idx"], aux["topk_gate"] = idx, gate
     xb = x.view(torch.bfloat16)
     acc = None
     for s in range(0 if layer.shared is None else layer.desc.n_shared):
         g, u, d = (m[s] for m in layer.shared)
-        linear(xb, g, ws, act="silu", w_mul=u, out=bufs["shared_h"], stream=stream)
-        acc = linear(bufs["shared_h"], d, ws, residual=acc, out=bufs["shared_y"], stream=stream)
-    sort_pairs(idx, layer.desc.n_experts, bufs["sort_ws"], bufs["pos"], bufs["order"], bufs["offsets"], stream=stream)
-    permute_rows(xb, bufs["pos"], out=bufs["rows"], stream=stream)
-    grouped_linear(bufs["rows"], bufs["offsets"], layer.w_gate, ws, act="silu", w_mul=layer.w_up, out=bufs["h"],
-                   stream=stream)
-    grouped_linear(bufs["h"], bufs["offsets"], layer.w_down, ws, out=bufs["z"], stream=stream)
-    unpermute_rows(bufs["z"], bufs["pos"], gate, residual=acc, out=y, stream=stream)
+        linear(xb, g, ws, act="silu", w_mul=u, out=bufs["shared_h"])
+        acc = linear(bufs["shared_h"], d, ws, residual=acc, out=bufs["shared_y"])
+    sort_pairs(idx, layer.desc.n_experts, bufs["sort_ws"], bufs["pos"], bufs["order"], bufs["offsets"])
+    permute_rows(xb, bufs["pos"], out=bufs["rows"])
+    grouped_linear(bufs["rows"], bufs["offsets"], layer.w_gate, ws, act="silu", w_mul=layer.w_up, out=bufs["h"])
+    grouped_linear(bufs["h"], bufs["offsets"], layer.w_down, ws, out=bufs["z"])
+    unpermute_rows(bufs["z"], bufs["pos"], gate, residual=acc, out=y)
     return y
 
 

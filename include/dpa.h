@@ -456,7 +456,7 @@ dpa_status dpa_sort_pairs(const int32_t* idx, int n_pairs, int n_experts, int32_
 /* out[pos[t][k]] = x[t] (device). x [n_tokens][hidden], out [n_tokens*top_k][hidden], both of
  * `dtype` (bf16, fp16, fp32); pos int32 [n_tokens][top_k] with distinct places, as dpa_sort_pairs
  * writes them. Places outside [0, n_tokens*top_k) are skipped; rows of out that no pair takes are
- * left as they were. Any hidden >= 1; top_k <= 32; n_tokens*top_k <= 2^30 (all row calls).
+ * left as they were. Any hidden in 1 .. 2^24; top_k <= 32; n_tokens*top_k <= 2^30 (all row calls).
  * Gradient: dpa_unpermute_rows without weights. */
 dpa_status dpa_permute_rows(int dtype, const void* x, const int32_t* pos, int n_tokens, int top_k, int hidden,
                             void* out, void* stream);
@@ -486,7 +486,8 @@ dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z,
  * (`dtype` or fp32); residual [rows][out_features] of residual_dtype (out_dtype or fp32), may be out
  * itself. bias, w_mul, bias_mul, residual may be
  * NULL. Products are summed in fp32; out is rounded once. gelu is v*Phi(v), gelu_tanh its tanh
- * form. in_features must be a multiple of 8; any rows and out_features >= 1.
+ * form. in_features must be a multiple of 8, at most 2^22; any rows and
+ * out_features >= 1. out overlaps no input but the residual.
  * ws: device, zero-filled once, at least DPA_LINEAR_WORKSPACE_BYTES (any workspace of this
  * library serves); it receives the device error flag only. */
 #define DPA_LINEAR_WORKSPACE_BYTES 256

@@ -54,6 +54,7 @@ def test_row_call_arguments():
             assert f(**bad) == 1, bad
         assert f(K=33) == 2
         assert f(T=1 << 28, K=8) == 2
+        assert f(H=(1 << 24) + 1) == 2
     assert permute(x=None) == 1 and permute(x=ODD) == 1 and permute(out=None) == 1 and permute(out=ODD) == 1
     for bad in (dict(z=None), dict(y=None), dict(z=ODD), dict(y=ODD), dict(res=ODD), dict(w=ODD), dict(wt=0),
                 dict(wt=1), dict(odt=1), dict(odt=3), dict(dtype=1, odt=0),
@@ -78,7 +79,7 @@ def test_product_arguments(groups):
         return linear(groups=groups, **kw)
 
     for desc, code in (((0, 64, 32, 0, 0, 0), 1), ((4, 0, 32, 0, 0, 0), 1), ((4, 64, 0, 0, 0, 0), 1),
-                       ((4, 60, 32, 0, 0, 0), 2), ((4, 64, 32, 2, 2, 0), 1), ((4, 64, 32, 0, 1, 0), 1),
+                       ((4, 60, 32, 0, 0, 0), 2), ((4, (1 << 22) + 8, 32, 0, 0, 0), 2), ((4, 64, 32, 2, 2, 0), 1), ((4, 64, 32, 0, 1, 0), 1),
                        ((4, 64, 32, 1, 0, 0), 1), ((4, 64, 32, 0, 3, 0), 1), ((4, 64, 32, 0, 0, 5), 1),
                        ((4, 64, 32, 0, 0, -1), 1)):
         assert f(desc=desc) == code, desc

@@ -193,6 +193,22 @@ def test_rows_skip_places_outside_the_rows():
     assert torch.equal((dz != 0).any(1).nonzero()[:, 0].cpu(), torch.sort(pos[ok]).values.long().cpu())
 
 
+def test_gates_of_unrouted_pairs_are_not_used():
+    T, K, H = 40, 4, 264
+    _, pos, _, live = sorted_rows(T, K, 8, 0.4, 2)
+    g = gen(5)
+    z, dy = normal(g, T * K, H), normal(g, T, H)
+    w = torch.rand((T, K), generator=g, device="cuda")
+    bad = torch.where(pos >= 0, w, float("nan"))
+    assert torch.equal(dpa.unpermute_rows(z, pos, bad), dpa.unpermute_rows(z, pos, w))
+    big = dict(z=z.repeat(200, 1), pos=pos.repeat(200, 1), w=bad.repeat(200, 1))    # the streaming kernel
+    y = dpa.unpermute_rows(big["z"], big["pos"], big["w"])
+    assert torch.equal(y[:T], dpa.unpermute_rows(z, pos, w)) and torch.equal(y[-T:], y[:T])
+    dy[3] = float("inf")
+    _, dw = dpa.unpermute_rows_backward(dy, z, pos, bad)
+    assert bool((dw[pos < 0] == 0).all())
+
+
 def test_rows_infinities_stay_in_their_tokens():
     T, K, H = 9, 3, 256
     _, pos, _, _ = sorted_rows(T, K, 8, 0.0, 1)
@@ -447,6 +463,34 @@ def test_product_nan_and_infinity_stay_in_their_rows_and_features():
     assert torch.equal(z.float(), torch.zeros_like(z.float()))    # far negative: 0, not NaN
 
 
+@pytest.mark.parametrize("rows", [5, 70, 400])
+def test_products_write_outputs_that_start_on_16_bytes(rows):
+    # the least alignment that the calls accept, for every buffer; what lies around stays
+    K, N = 136, 4808
+    g = gen(rows)
+    dt = torch.bfloat16
+
+    def shifted(t):
+        flat = torch.full((t.numel() + 64,), 3.0, dtype=t.dtype, device="cuda")
+        at = 16 // t.element_size()
+        flat[at:at + t.numel()] = t.reshape(-1)
+        return flat, flat[at:at + t.numel()].view(t.shape)
+
+    x, w, _, b, _, _ = product_inputs(g, rows, K, N, dt, False, True, False, dt)
+    _, xs = shifted(x)
+    _, ws_ = shifted(w)
+    _, bs = shifted(b)
+    for odt in (torch.float32, dt):
+        r = normal(g, rows, N, dtype=odt)
+        flat, out = shifted(r)
+        assert out.data_ptr() % 32 == 16
+        dpa.linear(xs, ws_, dpa.new_linear_workspace(), bias=bs, act="silu", residual=out, out=out)
+        ref, tol = product64(x, w, b, "silu", None, None, r, odt)
+        close(out, ref, tol)
+        at = 16 // r.element_size()
+        assert bool((flat[:at] == 3.0).all()) and bool((flat[at + r.numel():] == 3.0).all())
+
+
 def test_linear_past_32_bit_offsets():
     rows, K, N = 270000, 8, 8192
     g = gen(7)
@@ -559,6 +603,8 @@ def test_refusals_on_the_device():
     with pytest.raises(dpa.DpaError) as err:
         dpa.linear(x[:, :12].contiguous(), w[:, :12].contiguous(), ws)
     assert err.value.status == 2
+    with pytest.raises(ValueError):
+        dpa.linear(x.int(), w, ws)
     with pytest.raises(dpa.DpaError) as err:
         dpa.linear(x, w, ws[:128])
     assert err.value.status == 3
