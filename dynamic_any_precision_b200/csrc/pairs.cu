@@ -393,11 +393,14 @@ __global__ void __launch_bounds__(256) unpermute_kernel(UnpermuteArgs a, int wpt
 // being kStreamPieces times 32 packs, and keeps the next items' rows on their way into shared
 // memory (asynchronous copies into a ring of its own, nothing shared between threads), so that the
 // loads in flight do not depend on registers. An item's rows are its token's routed slots only,
-// kStreamRows at a time.
-constexpr int kStreamThreads = 128, kStreamStages = 3, kStreamRows = 4, kStreamPieces = 2, kStreamCtas = 3;   // CTAs per SM
+// kStreamRows at a time. (Bound by latency with few warps and by copies in flight with small rings:
+// 16384 tokens of 8 bf16 rows take 92 to 100 us over one to two runs of packs, two to four rows and
+// two or three stages; where a third of the slots is routed, two rows at a time and seven CTAs per SM
+// are 10% ahead of four rows and three CTAs.)
+constexpr int kStreamThreads = 128, kStreamStages = 3, kStreamRows = 2, kStreamPieces = 2;
 constexpr int kStreamPack = kStreamThreads * 16;
 constexpr int kStreamRes = kStreamRows * kStreamPieces * kStreamPack;        // residual packs behind the rows'
-constexpr int kStreamStage = kStreamRes + kStreamPieces * kStreamThreads * 32;
+constexpr int kStreamSmem = 227 * 1024, kStreamMaxCtas = 7;                     // per SM
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
@@ -443,7 +446,8 @@ struct Cursor {
 };
 
 template <typename ZT, typename YT, typename RT>
-__global__ void __launch_bounds__(kStreamThreads, kStreamCtas) unpermute_stream_kernel(UnpermuteArgs a, int runs) {
+__global__ void __launch_bounds__(kStreamThreads, kStreamMaxCtas) unpermute_stream_kernel(UnpermuteArgs a, int runs,
+                                                                                          int stage_bytes) {
     constexpr int VEC = 16 / sizeof(ZT), kRes = VEC * sizeof(RT);
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_wait();
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) unpermute_stream_
     auto issue = [&](int stage) {
         if (in.left > 0) {
             const int c = (in.run * kStreamPieces * 32 + lane) * VEC;
-            const uint32_t dst = base + stage * kStreamStage;
+            const uint32_t dst = base + stage * stage_bytes;
 #pragma unroll
             for (int u = 0; u < kStreamRows; ++u) {
                 if (in.s0 + u < in.n) {
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) unpermute_stream_
         asm volatile("cp.async.wait_group %0;" ::"n"(kStreamStages - 2) : "memory");
         issue(stage == 0 ? kStreamStages - 1 : stage - 1);   // the stage used up by the last round
         const int c = (out.run * kStreamPieces * 32 + lane) * VEC;
-        const unsigned char* src = ring + stage * kStreamStage;
+        const unsigned char* src = ring + stage * stage_bytes;
 #pragma unroll
         for (int u = 0; u < kStreamRows; ++u) {
             if (out.s0 + u < out.n) {
@@ -664,17 +668,21 @@ cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream, int sms
     UnpermuteArgs b = a;
     constexpr int kRun = kStreamPieces * 32 * kWidest;
     const int runs = (a.H - 1) / kRun + 1;
-    const int ctas = kStreamCtas * sms;
-    // two items per warp at least (1024 tokens of 8 rows of 2048 bf16: 7.5 us, against 8.9 us for the
-    // kernel without the ring; 4096 tokens: 27 against 40 us)
-    if (vec == kWidest && static_cast<int64_t>(a.T) * runs >= static_cast<int64_t>(ctas) * (kStreamThreads / 32) * 2) {
+    int stage_bytes = kStreamRes + (a.residual ? kStreamPieces * kStreamThreads * kWidest * static_cast<int>(sizeof(RT)) : 0);
+    const int smem = kStreamStages * stage_bytes;
+    int per_sm = kStreamSmem / (smem + 1024);   // the system takes 1 KB of each CTA's
+    per_sm = per_sm < kStreamMaxCtas ? per_sm : kStreamMaxCtas;
+    // two items per warp at least, and two CTAs per SM (8 rows of 2048 bf16 per token: at 512 tokens 5.5
+    // us with the ring, 5.0 without; at 1024 tokens 8.0 and 13.2, at 4096 26.6 and 40.8)
+    const int64_t fed = static_cast<int64_t>(a.T) * runs / (kStreamThreads / 32 * 2);
+    if (vec == kWidest && fed >= 2 * sms) {
+        const int ctas = fed < per_sm * sms ? static_cast<int>(fed) : per_sm * sms;
         const void* fn = reinterpret_cast<const void*>(unpermute_stream_kernel<ZT, YT, RT>);
-        const size_t smem = static_cast<size_t>(kStreamStages) * kStreamStage;
-        const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
         int r = runs;
-        void* sargs[] = {&b, &r};
-        return launch_pdl_raw(fn, dim3(ctas), dim3(kStreamThreads), smem, stream, sargs);
+        void* sargs[] = {&b, &r, &stage_bytes};
+        return launch_pdl_raw(fn, dim3(ctas), dim3(kStreamThreads), static_cast<size_t>(smem), stream, sargs);
     }
     void* args[] = {&b, &wpt};
     const void* fn = vec == kWidest ? reinterpret_cast<const void*>(unpermute_kernel<ZT, YT, RT, kWidest>)
