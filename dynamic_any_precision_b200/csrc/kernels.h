@@ -283,9 +283,8 @@ struct LinearArgs {
 };
 cudaError_t launch_linear(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
                           cudaStream_t stream, int sms);
-// The plain product for at most kFewRows rows (linear_few.cu).
-constexpr int kFewRows = 32;
+// The products of few rows (linear_few.cu): at most 32 plain ones, or any that lie in few per group.
 cudaError_t launch_linear_few(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
-                              cudaStream_t stream);
+                              cudaStream_t stream, int sms);
 
 }  // namespace dpa

@@ -363,7 +363,8 @@ def product_inputs(g, rows, K, N, dt, gated, bias, residual, odt, lead=()):
 LINEAR = [
     (1, 8, 1, "none", False, False, False), (1, 2048, 2048, "none", False, True, True),
     (1, 64, 64, "silu", True, True, False), (3, 72, 7, "relu", False, True, False),
-    (16, 200, 129, "gelu", False, False, True), (17, 768, 300, "gelu_tanh", False, True, True),
+    (16, 200, 129, "gelu", False, False, True), (9, 4104, 200, "silu", True, True, True), (24, 1000, 2000, "none", False, True, False),
+    (31, 2048, 2050, "silu", True, True, False), (2, 520, 9000, "gelu_tanh", False, True, True), (17, 768, 300, "gelu_tanh", False, True, True),
     (64, 2048, 2816, "silu", True, False, False), (100, 136, 65, "none", True, True, True),
     (128, 64, 128, "none", False, False, False), (129, 1408, 2048, "none", False, False, True),
     (200, 4096, 33, "silu", True, True, False), (300, 320, 1000, "relu", True, False, False),
@@ -396,7 +397,8 @@ def test_linear(rows, K, N, act, gated, bias, residual, dtype, out):
 
 # rows per group, K, N, act, gated, bias, residual
 GROUPED = [
-    ([1], 64, 64, "none", False, False, False), ([0, 0, 0], 64, 64, "none", False, True, False),
+    ([1], 64, 64, "none", False, False, False), ([0] * 70 + [40, 0, 3, 20] + [0] * 30, 1032, 90, "silu", True, True, True),
+    ([0] * 1000 + [2] * 24, 264, 33, "gelu", False, True, True), ([8] * 2, 520, 129, "relu", False, False, True), ([0, 0, 0], 64, 64, "none", False, True, False),
     ([0, 5, 0, 1, 0], 72, 7, "relu", False, True, True), ([1] * 8 + [0] * 120, 2048, 768, "silu", True, False, False),
     ([4] * 128, 256, 200, "silu", True, True, True), ([300, 1, 0, 17, 128, 129], 200, 330, "gelu", False, True, False),
     ([40] * 3, 512, 65, "gelu_tanh", True, True, False), ([100] * 16, 136, 1500, "none", False, True, True),
