@@ -16,6 +16,7 @@ bool opt16(const void* p) { return !p || aligned16(p); }    // optional, aligned
 
 constexpr int64_t kMaxPairs = 1 << 30;
 constexpr int kMaxRowLength = 1 << 24;   // row calls: 32-bit positions inside a row
+constexpr int kMaxSide = 1 << 30;        // products: rows and output features, in 32 bits with a tile's overhang
 constexpr int kMaxInputs = 1 << 22;      // products: a tile's K loop stays far below the kernels' time limit
 
 bool row_type(int t) { return t == DPA_DTYPE_BF16 || t == DPA_DTYPE_FP16 || t == DPA_DTYPE_FP32; }
@@ -52,6 +53,7 @@ dpa_status run_linear(const dpa_linear_desc* d, int groups, const void* x, const
     if (!opt16(bias) || !opt16(w_mul) || !opt16(bias_mul) || !opt16(residual)) return DPA_ERR_INVALID_ARG;
     if (bias_mul && !w_mul) return DPA_ERR_INVALID_ARG;
     if (d->in_features % 8 || d->in_features > kMaxInputs) return DPA_ERR_UNSUPPORTED;   // rows of whole 16-byte pieces (tensor loads)
+    if (d->rows > kMaxSide || d->out_features > kMaxSide) return DPA_ERR_UNSUPPORTED;
     if (ws_bytes < DPA_LINEAR_WORKSPACE_BYTES) return DPA_ERR_WORKSPACE;
     dpa::LinearArgs a{};
     a.rows = d->rows;

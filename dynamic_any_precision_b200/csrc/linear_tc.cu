@@ -101,8 +101,9 @@ __device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref
     return t;
 }
 
-// Eight consecutive outputs (or residual values) of one token. `vec`: rows of whole 8-feature groups (N % 8 == 0, so that
-// every group is 16-byte aligned and wholly inside or outside N); otherwise `cnt` single elements.
+// Eight consecutive outputs (or residual values) of one token. `vec`: rows of whole 8-feature groups
+// (N % 8 == 0, so that every group is 16-byte aligned and wholly inside or outside N); otherwise `cnt`
+// single elements.
 struct Out8 {
     uint4 lo, hi;   // 16-bit values: lo only; fp32: lo, hi
 };
@@ -749,8 +750,10 @@ int cluster_capacity(int S) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1)
-            n = -1;
+            cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+            n = -1;   // K is not split then
+            (void)cudaGetLastError();
+        }
     }
     return n;
 }

@@ -33,7 +33,7 @@ constexpr int kSortOneBlock = 2048;   // pairs that one CTA sorts alone (one lau
 constexpr int kSortChunk = 1024;
 
 __device__ __forceinline__ int pair_key(const int32_t* idx, int p, int E) {
-    const int e = __ldg(idx + p);
+    const int e = __ldcg(idx + p);   // from L2: sort_place_kernel starts before sort_count_kernel ends
     return static_cast<unsigned>(e) < static_cast<unsigned>(E) ? e : E;
 }
 
@@ -247,7 +247,7 @@ __device__ __forceinline__ Slots load_slots(const int32_t* pos, const void* weig
 
 // A pack if `on`, else zeros. Written as predicated loads so that the loads of several rows stay
 // together in front of the arithmetic (as branches they were moved to their uses, one at a time:
-// 136 instead of 23 us for 4096 tokens of 8 rows of 2048 bf16).
+// 136 against 41 us for 4096 tokens of 8 rows of 2048 bf16).
 template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_if(const T* p, bool on) {
     constexpr int kBytes = sizeof(T) * VEC;
@@ -565,8 +565,10 @@ __device__ __forceinline__ float warp_sums8(const float (&v)[8], int lane) {
 // `wpt` warps per token (8 / wpt tokens per CTA). Each thread reads its part of dy and the same part
 // of up to 8 slots' rows, writes the rows' gradients and adds to their dot products; the dot
 // products are then summed over the lanes and, in order, over the token's warps.
+// Three CTAs per SM: two of them leave too few loads in flight (4096 tokens of 8 rows of 2048: fp32 109
+// against 93 us, bf16 50 against 49).
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) unpermute_bwd_kernel(UnpermuteBwdArgs a, int wpt) {
+__global__ void __launch_bounds__(256, 3) unpermute_bwd_kernel(UnpermuteBwdArgs a, int wpt) {
     constexpr int U = pieces(VEC);
     __shared__ float s_dot[8][8];
     pdl_wait();

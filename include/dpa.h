@@ -486,8 +486,8 @@ dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z,
  * (`dtype` or fp32); residual [rows][out_features] of residual_dtype (out_dtype or fp32), may be out
  * itself. bias, w_mul, bias_mul, residual may be
  * NULL. Products are summed in fp32; out is rounded once. gelu is v*Phi(v), gelu_tanh its tanh
- * form. in_features must be a multiple of 8, at most 2^22; any rows and
- * out_features >= 1. out overlaps no input but the residual.
+ * form. in_features must be a multiple of 8, at most 2^22; rows
+ * and out_features in 1 .. 2^30. out overlaps no input but the residual.
  * ws: device, zero-filled once, at least DPA_LINEAR_WORKSPACE_BYTES (any workspace of this
  * library serves); it receives the device error flag only. */
 #define DPA_LINEAR_WORKSPACE_BYTES 256

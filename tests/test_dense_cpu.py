@@ -79,7 +79,8 @@ def test_product_arguments(groups):
         return linear(groups=groups, **kw)
 
     for desc, code in (((0, 64, 32, 0, 0, 0), 1), ((4, 0, 32, 0, 0, 0), 1), ((4, 64, 0, 0, 0, 0), 1),
-                       ((4, 60, 32, 0, 0, 0), 2), ((4, (1 << 22) + 8, 32, 0, 0, 0), 2), ((4, 64, 32, 2, 2, 0), 1), ((4, 64, 32, 0, 1, 0), 1),
+                       ((4, 60, 32, 0, 0, 0), 2), ((4, (1 << 22) + 8, 32, 0, 0, 0), 2),
+                       (((1 << 30) + 1, 64, 32, 0, 0, 0), 2), ((4, 64, (1 << 30) + 1, 0, 0, 0), 2), ((4, 64, 32, 2, 2, 0), 1), ((4, 64, 32, 0, 1, 0), 1),
                        ((4, 64, 32, 1, 0, 0), 1), ((4, 64, 32, 0, 3, 0), 1), ((4, 64, 32, 0, 0, 5), 1),
                        ((4, 64, 32, 0, 0, -1), 1)):
         assert f(desc=desc) == code, desc

@@ -96,6 +96,20 @@ def test_sort_pairs_one_expert_takes_all():
     assert offsets.cpu().tolist() == [0] * 6 + [36000] * 4
 
 
+def test_sort_pairs_of_ids_written_just_before():
+    # several chunks: the second kernel starts before the first has ended, on ids that the kernel
+    # before both of them has written; nothing waits between the rounds
+    T, K, E = 9000, 4, 96
+    rounds = [torch.from_numpy(routing(T, K, E, s, 0.1)).cuda() for s in range(12)]
+    idx, ws, got = torch.empty_like(rounds[0]), dpa.new_sort_workspace(T * K, E), []
+    for r in rounds:
+        idx.copy_(r)
+        got.append(dpa.sort_pairs(idx, E, ws))
+    for r, g in zip(rounds, got):
+        for a, b in zip(g, host_sort(r.cpu().numpy(), E)):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+
 def test_sort_workspace_of_a_longer_batch_serves_shorter_ones():
     ws = dpa.new_sort_workspace(131073, 16)
     for P in (131073, 131072, 131071, 9000, 4097, 4096, 1):
@@ -579,6 +593,35 @@ def test_bf16_bit_tensors_and_streams():
         c = dpa.linear(x, w, ws)
     stream.synchronize()
     assert b.dtype == torch.int16 and torch.equal(b.view(torch.bfloat16), y) and torch.equal(c, y)
+
+
+def test_calls_on_two_streams_at_once():
+    g = gen(31)
+    T, K, E, H, N = 3000, 4, 16, 512, 1100
+    dt = torch.bfloat16
+    idx = torch.from_numpy(routing(T, K, E, 8, 0.1)).cuda()
+    x, w = normal(g, T, H, dtype=dt), normal(g, E, N, H, dtype=dt, scale=H ** -0.5)
+    gates = torch.rand((T, K), generator=g, device="cuda")
+
+    def chain(sort_ws, ws, n):
+        for _ in range(n):
+            pos, _, off = dpa.sort_pairs(idx, E, sort_ws)
+            rows = dpa.permute_rows(x, pos, out=torch.zeros((T * K, H), dtype=dt, device="cuda"))
+            z = dpa.grouped_linear(rows, off, w, ws, act="silu", out=torch.zeros((T * K, N), dtype=dt, device="cuda"))
+            y = dpa.unpermute_rows(z, pos, gates)
+        return y
+
+    spaces = [(dpa.new_sort_workspace(T * K, E), dpa.new_linear_workspace()) for _ in range(3)]
+    want = chain(*spaces[2], 1)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s, sp in zip(streams, spaces):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(chain(*sp, 6))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], want)
+    assert all(dpa.device_status(ws) == 0 for _, ws in spaces)
 
 
 def test_refusals_on_the_device():
