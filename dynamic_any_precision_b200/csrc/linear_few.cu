@@ -68,7 +68,7 @@ __device__ __forceinline__ bool nonempty_group(const LinearArgs& a, int i, int l
 
 // NT tiles of 8 tokens at a time; MATS weight matrices (2: gated). Grid: feature blocks, groups (at
 // most as many as there are rows).
-template <bool F16, int MATS, int NT, bool GROUPED, int kWarps>
+template <bool F16, int MATS, int NT, bool GROUPED, int kWarps, bool PRECISE>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == 16 ? 1 : (NT == 1 ? 3 : 2) * 8 / kWarps) few_rows_kernel(LinearArgs a, const uint16_t* x, const uint16_t* w,
                                                                const uint16_t* u) {
     __shared__ float s_part[kWarps][MATS][8 * NT][kFeat + 1];
@@ -112,16 +112,33 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 16 ? 1 : (NT == 1 ? 3 :
                                    : make_uint4(0, 0, 0, 0);
                 }
             }
+            auto multiply = [&](float (&sum)[MATS][NT][4]) {   // in the order of the loads
 #pragma unroll
-            for (int i = 0; i < kRound; ++i)
+                for (int i = 0; i < kRound; ++i)
+#pragma unroll
+                    for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const uint4 p = av[i][m][0], q = av[i][m][1], s = bv[i][t];
+                            mma16<F16>(sum[m][t], p.x, q.x, p.y, q.y, s.x, s.y);
+                            mma16<F16>(sum[m][t], p.z, q.z, p.w, q.w, s.z, s.w);
+                        }
+            };
+            if constexpr (PRECISE) {
+                // fp32 outputs: a round's products are summed by themselves and added with rounding;
+                // the MMA drops the bits below its accumulator's last place at every step, which
+                // would grow with K
+                float part[MATS][NT][4] = {};
+                multiply(part);
 #pragma unroll
                 for (int m = 0; m < MATS; ++m)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const uint4 p = av[i][m][0], q = av[i][m][1], s = bv[i][t];
-                        mma16<F16>(acc[m][t], p.x, q.x, p.y, q.y, s.x, s.y);
-                        mma16<F16>(acc[m][t], p.z, q.z, p.w, q.w, s.z, s.w);
-                    }
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][t][i] += part[m][t][i];
+            } else {
+                multiply(acc);
+            }
         }
         if (GROUPED && t0 > 0) __syncthreads();   // the last tile's sums have been read
 #pragma unroll
@@ -151,21 +168,28 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 16 ? 1 : (NT == 1 ? 3 :
     }
 }
 
+template <bool F16, int MATS, int NT, bool GROUPED, int WARPS>
+const void* pick_kernel(bool precise) {
+    return precise ? reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, NT, GROUPED, WARPS, true>)
+                   : reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, NT, GROUPED, WARPS, false>);
+}
+
 template <bool F16, int MATS, int WARPS>
-const void* pick_tokens(bool grouped, int tokens) {
-    // groups of so few rows have one or two each; more take turns
-    if (grouped) return reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 1, true, WARPS>);
-    if (tokens <= 8) return reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 1, false, WARPS>);
-    if (tokens <= 16) return reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 2, false, WARPS>);
-    return reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 4, false, WARPS>);
+const void* pick_tokens(bool grouped, int tokens, bool precise) {
+    if constexpr (WARPS < 16) {
+        // groups of so few rows have one or two each; more take turns
+        if (grouped) return pick_kernel<F16, MATS, 1, true, WARPS>(precise);
+        if (tokens > 16) return pick_kernel<F16, MATS, 4, false, WARPS>(precise);
+    }
+    return tokens <= 8 ? pick_kernel<F16, MATS, 1, false, WARPS>(precise)
+                       : pick_kernel<F16, MATS, 2, false, WARPS>(precise);
 }
 
 template <bool F16, int MATS>
-const void* pick(bool grouped, int tokens, int warps) {
-    if (warps == 16)
-        return tokens <= 8 ? reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 1, false, 16>)
-                           : reinterpret_cast<const void*>(few_rows_kernel<F16, MATS, 2, false, 16>);
-    return warps == 4 ? pick_tokens<F16, MATS, 4>(grouped, tokens) : pick_tokens<F16, MATS, 8>(grouped, tokens);
+const void* pick(bool grouped, int tokens, int warps, bool precise) {
+    return warps == 16  ? pick_tokens<F16, MATS, 16>(grouped, tokens, precise)
+           : warps == 8 ? pick_tokens<F16, MATS, 8>(grouped, tokens, precise)
+                        : pick_tokens<F16, MATS, 4>(grouped, tokens, precise);
 }
 
 }  // namespace
@@ -181,8 +205,9 @@ cudaError_t launch_linear_few(const LinearArgs& a, bool f16, const void* x, cons
     const int64_t ctas = static_cast<int64_t>(blocks) * groups;
     int warps = ctas <= 3 * sms && a.K > 512 ? 8 : 4;
     if (!grouped && ctas <= sms && a.K > 1024 && a.rows <= 16) warps = 16;
-    const void* fn = w_mul ? (f16 ? pick<true, 2>(grouped, a.rows, warps) : pick<false, 2>(grouped, a.rows, warps))
-                           : (f16 ? pick<true, 1>(grouped, a.rows, warps) : pick<false, 1>(grouped, a.rows, warps));
+    const bool precise = a.out32;
+    const void* fn = w_mul ? (f16 ? pick<true, 2>(grouped, a.rows, warps, precise) : pick<false, 2>(grouped, a.rows, warps, precise))
+                           : (f16 ? pick<true, 1>(grouped, a.rows, warps, precise) : pick<false, 1>(grouped, a.rows, warps, precise));
     LinearArgs b = a;
     void* args[] = {&b, &x, &w, &w_mul};
     return launch_pdl_raw(fn, dim3(blocks, groups), dim3(warps * 32), 0, stream, args);

@@ -21,9 +21,9 @@
 //
 // Roles (576 threads): warps 0-15 epilogue (four per TMEM lane quadrant; with eight, an epilogue of
 // 256 tokens took longer than 2048 inputs' MMAs), warp 16 TMA loads (no multicast), warp 17 TMEM
-// allocation and MMA issue. Two accumulators of 256 columns alternate, so
-// a tile's epilogue overlaps the next tile's MMAs. Every wait is bounded: on a timeout the kernel
-// records DPA_ERR_DEVICE_TIMEOUT and every role leaves its loop.
+// allocation and MMA issue. Two accumulators alternate, so that a tile's epilogue (or a K block's
+// addition to the running sums) overlaps the next one's MMAs. Every wait is bounded: on a timeout the
+// kernel records DPA_ERR_DEVICE_TIMEOUT and every role leaves its loop.
 #include <mutex>
 
 #include <cuda_bf16.h>
@@ -45,7 +45,8 @@ constexpr int kChunk = 16;                       // tokens that a group finishes
 constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kThreads = (kEpiWarps + 2) * 32;   // 576
 constexpr int kMaxStages = 12;
-constexpr uint32_t kTmemCols = 512, kAccCols = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kBlockedSteps = 4, kBlockedTokens = 160;   // K in blocks: steps per block, most tokens per tile
 constexpr int kSmemMax = 232448;
 constexpr int kOutBytes = kGroups * kChunk * kRowsA * 4;   // epilogue staging, one chunk per group
 // full[stages], empty[stages], acc_full[2], acc_empty[2], done; then the TMEM address and abort flag
@@ -320,11 +321,12 @@ __device__ __forceinline__ void load_sums(const float* p0, const float* p1, Two 
     v[3] = two(y.z, y.w);
 }
 
-template <int CG, bool GATED, bool F16>
+template <int CG, bool GATED, bool F16, bool BLOCKED>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ CUtensorMap umap,
                                                              const __grid_constant__ RowMaps xmaps) {
     constexpr int kFeat = GATED ? 64 : 128;   // output features per CTA
+    constexpr int kAccCols = BLOCKED ? kBlockedTokens : 256;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
@@ -470,37 +472,40 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             const bool leader = elect_one();
             const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB);
             const uint64_t dconst = smem_desc_sw128(0);
-            int s = 0, ph = 0, j = 0;
+            int s = 0, ph = 0, j = 0;   // j: accumulators filled
             bool ok = true;
-            for (int it = cid; it < ntiles && ok; it += ncl, ++j) {
+            for (int it = cid; it < ntiles && ok; it += ncl) {
                 const Tile t = find_tile<CG>(a, s_pref, it);
-                const int b = j & 1;
                 const int ncols = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
                 const uint32_t idesc = instr_desc(F16 ? 0 : 1, ncols, 128 * CG);
-                const uint32_t td = tmem + static_cast<uint32_t>(b) * kAccCols;
-                bool w_ok = mbar_wait_abortable(&acc_empty[b], ((j >> 1) & 1) ^ 1, s_abort, a.hdr, 0x720);
-                if (!__all_sync(0xffffffffu, w_ok)) break;
-                for (int kc = k0; kc < k1; ++kc) {
-                    w_ok = mbar_wait_abortable(&full[s], ph, s_abort, a.hdr, 0x721);
-                    if (!__all_sync(0xffffffffu, w_ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = dconst | ((a_base + static_cast<uint32_t>(s) * kATile) >> 4);
-                    const uint64_t bd = dconst | ((b_base + static_cast<uint32_t>(s * btile)) >> 4);
-                    if (leader) {
-                        mma_f16<CG>(td, ad, bd, idesc, kc > k0 ? 1u : 0u);
-                        mma_f16<CG>(td, ad + 2, bd + 2, idesc, 1u);
-                        mma_f16<CG>(td, ad + 4, bd + 4, idesc, 1u);
-                        mma_f16<CG>(td, ad + 6, bd + 6, idesc, 1u);
-                        commit<CG>(&empty[s]);
-                        if (kc == k1 - 1) commit<CG>(&acc_full[b]);
-                    }
-                    __syncwarp();
-                    if (++s == stages) {
-                        s = 0;
-                        ph ^= 1;
+                for (int kb = k0, kend; kb < k1 && ok; kb = kend, ++j) {
+                    const int b = j & 1;
+                    kend = BLOCKED ? min(kb + kBlockedSteps, k1) : k1;
+                    const uint32_t td = tmem + static_cast<uint32_t>(b * kAccCols);
+                    bool w_ok = mbar_wait_abortable(&acc_empty[b], ((j >> 1) & 1) ^ 1, s_abort, a.hdr, 0x720);
+                    ok = __all_sync(0xffffffffu, w_ok);
+                    for (int kc = kb; kc < kend && ok; ++kc) {
+                        w_ok = mbar_wait_abortable(&full[s], ph, s_abort, a.hdr, 0x721);
+                        if (!__all_sync(0xffffffffu, w_ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = dconst | ((a_base + static_cast<uint32_t>(s) * kATile) >> 4);
+                        const uint64_t bd = dconst | ((b_base + static_cast<uint32_t>(s * btile)) >> 4);
+                        if (leader) {
+                            mma_f16<CG>(td, ad, bd, idesc, kc > kb ? 1u : 0u);
+                            mma_f16<CG>(td, ad + 2, bd + 2, idesc, 1u);
+                            mma_f16<CG>(td, ad + 4, bd + 4, idesc, 1u);
+                            mma_f16<CG>(td, ad + 6, bd + 6, idesc, 1u);
+                            commit<CG>(&empty[s]);
+                            if (kc == kend - 1) commit<CG>(&acc_full[b]);
+                        }
+                        __syncwarp();
+                        if (++s == stages) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
                 }
             }
@@ -537,10 +542,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         }
         const bool vec = (a.N & 7) == 0;
         if (CG == 1 && S > 1) cluster_wait();   // every CTA of the cluster has started
+        auto release = [&](int b) {   // this warp has read its part of accumulator b
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) arrive_cluster(empty_bar[b]);
+                else mbarrier_arrive(&acc_empty[b]);
+            }
+        };
+        const bool blocked = BLOCKED && k1 - k0 > kBlockedSteps;
+        const uint32_t sums = tmem + lane_base + static_cast<uint32_t>(2 * kAccCols);   // of a tile's K blocks
         int j = 0;
         for (int it = cid; it < ntiles; it += ncl, ++j) {
             const Tile t = find_tile<CG>(a, s_pref, it);
-            const int b = j & 1;
             const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + fg * 8;
             const int cnt = min(max(a.N - f, 0), 8);
             const int nch = (t.n + kChunk - 1) / kChunk;
@@ -559,20 +573,55 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                     }
                 }
             }
-            bool w_ok = mbar_wait_abortable(&acc_full[b], (j >> 1) & 1, s_abort, a.hdr, 0x730);
+            // every K block but the last: added to the running sums
+            bool w_ok = true;
+            for (int kb = k0; BLOCKED && kb + kBlockedSteps < k1; kb += kBlockedSteps, ++j) {
+                w_ok = mbar_wait_abortable(&acc_full[j & 1], (j >> 1) & 1, s_abort, a.hdr, 0x731);
+                w_ok = group_agree(grp, w_ok);
+                if (!w_ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + lane_base + static_cast<uint32_t>((j & 1) * kAccCols);
+                for (int c = grp; c < nch; c += kGroups) {
+                    uint32_t v[kChunk], w[kChunk];
+                    tmem_ld16(acc + kChunk * c, v);
+                    if (kb > k0) tmem_ld16(sums + kChunk * c, w);
+                    tmem_wait_ld();
+                    if (kb > k0) {
+#pragma unroll
+                        for (int u = 0; u < kChunk; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) + __uint_as_float(w[u]));
+                    }
+                    tmem_st16(sums + kChunk * c, v);
+                }
+                tmem_wait_st();
+                release(j & 1);
+            }
+            if (!w_ok) break;
+            const int b = j & 1;
+            w_ok = mbar_wait_abortable(&acc_full[b], (j >> 1) & 1, s_abort, a.hdr, 0x730);
             w_ok = group_agree(grp, w_ok);   // the group leaves together (it synchronises below)
             if (!w_ok) break;
             tc_fence_after();
-            const uint32_t acc = tmem + lane_base + static_cast<uint32_t>(b) * kAccCols;
+            const uint32_t acc = tmem + lane_base + static_cast<uint32_t>(b * kAccCols);
+            auto read_sums = [&](int c, uint32_t (&v)[kChunk]) {
+                tmem_ld16(acc + kChunk * c, v);
+                if (BLOCKED && blocked) {
+                    uint32_t w[kChunk];
+                    tmem_ld16(sums + kChunk * c, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < kChunk; ++u) v[u] = __float_as_uint(__uint_as_float(v[u]) + __uint_as_float(w[u]));
+                } else {
+                    tmem_wait_ld();
+                }
+            };
             if (CG == 1 && S > 1) {
                 // token u goes to CTA u mod S of the cluster: [this CTA's rank][u / S][128]
                 const int slice = (t.n + S - 1) / S * kRowsA;
                 const uint32_t dst = smem_u32(s_out) + static_cast<uint32_t>(rank * slice + R) * 4;
                 for (int c = grp; c < nch; c += kGroups) {
                     uint32_t v[kChunk];
-                    tmem_ld16(acc + kChunk * c, v);
+                    read_sums(c, v);
                     int place = kChunk * c / S, owner = kChunk * c - place * S;
-                    tmem_wait_ld();
 #pragma unroll
                     for (int u = 0; u < kChunk; ++u) {
                         if (kChunk * c + u < t.n)
@@ -587,16 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             }
             for (int c = grp; c < nch; c += kGroups) {
                 uint32_t v[kChunk];
-                tmem_ld16(acc + kChunk * c, v);
-                tmem_wait_ld();
-                if (c + kGroups >= nch) {   // last read of this accumulator by this warp
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CG == 2) arrive_cluster(empty_bar[b]);
-                        else mbarrier_arrive(&acc_empty[b]);
-                    }
-                }
+                read_sums(c, v);
+                if (c + kGroups >= nch) release(b);   // last read of this accumulator by this warp
                 if (c > grp) group_sync(grp);   // the chunk before has been read out
 #pragma unroll
                 for (int u = 0; u < kChunk; ++u) put[u * kRowsA] = __uint_as_float(v[u]);
@@ -621,12 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                     }
                 }
             }
-            if (grp >= nch) {   // this group had nothing to read
-                if (lane == 0) {
-                    if (CG == 2) arrive_cluster(empty_bar[b]);
-                    else mbarrier_arrive(&acc_empty[b]);
-                }
-            }
+            if (grp >= nch) release(b);   // this group had nothing to read
             group_sync(grp);   // read out before the next tile is staged
         }
     }
@@ -701,9 +737,10 @@ bool encode_map(CUtensorMap* map, const void* base, bool f16, uint64_t cols, uin
 }
 
 template <int CG, bool GATED, bool F16>
-cudaError_t launch_variant(LinearArgs& a, const CUtensorMap* wmaps, const RowMaps& xmaps, int clusters, size_t smem,
-                           cudaStream_t stream) {
-    const void* fn = reinterpret_cast<const void*>(linear_kernel<CG, GATED, F16>);
+cudaError_t launch_variant(LinearArgs& a, bool blocks, const CUtensorMap* wmaps, const RowMaps& xmaps, int clusters,
+                           size_t smem, cudaStream_t stream) {
+    const void* fn = blocks ? reinterpret_cast<const void*>(linear_kernel<CG, GATED, F16, true>)
+                            : reinterpret_cast<const void*>(linear_kernel<CG, GATED, F16, false>);
     const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (err != cudaSuccess) return err;
     const int csize = CG == 2 ? 2 : a.splits;
@@ -737,7 +774,7 @@ int cluster_capacity(int S) {
     std::lock_guard<std::mutex> lock(mu);
     int& n = known[dev][S];
     if (n == 0) {
-        const void* fn = reinterpret_cast<const void*>(linear_kernel<1, false, false>);
+        const void* fn = reinterpret_cast<const void*>(linear_kernel<1, false, false, false>);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(256 * S));
         cfg.blockDim = dim3(kThreads);
@@ -793,8 +830,15 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
     a.FT = (a.N - 1) / (feat * CG) + 1;
     a.splits = 1;
     int64_t clusters;
+    // K blocks: the tensor cores drop the bits below the accumulator's last place at every step of 16
+    // inputs, which takes about 1e-9 of the sum per input away (K = 8192: 9e-6; with a gate twice
+    // that). 16-bit outputs do not see it. For fp32 outputs of more than 768 inputs (512 with an
+    // activation, 256 with a gate, which widen the error) blocks of 256 are added in fp32 with
+    // rounding: 3e-7 whatever K. The running sums take a third of tensor memory, so a tile has at most
+    // 160 tokens then.
+    const bool blocks = a.out32 && a.ksteps > (gated ? 4 : a.act != DPA_ACT_NONE ? 8 : 12);
     if (a.E > 0) {
-        a.TN = pair ? 256 : 128;
+        a.TN = pair && !blocks ? 256 : 128;
         a.xbox = 16;
         // most token tiles there can be: every full tile, and one more per non-empty group
         const int64_t tiles =
@@ -803,7 +847,7 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
         if (!pair) a.splits = split_k(tiles, a.ksteps);
         clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
     } else {
-        a.TN = balanced_rows(a.rows, pair ? 256 : 128, 16 * CG);
+        a.TN = balanced_rows(a.rows, !pair ? 128 : blocks ? kBlockedTokens : 256, 16 * CG);
         a.xbox = a.TN / CG;
         const int64_t tiles = static_cast<int64_t>((a.rows - 1) / a.TN + 1) * a.FT;
         if (tiles > INT32_MAX) return cudaErrorInvalidValue;
@@ -830,15 +874,15 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
             return cudaErrorInvalidValue;
     const int c = static_cast<int>(clusters);
     if (pair) {
-        if (gated) return f16 ? launch_variant<2, true, true>(a, maps, xmaps, c, smem, stream)
-                              : launch_variant<2, true, false>(a, maps, xmaps, c, smem, stream);
-        return f16 ? launch_variant<2, false, true>(a, maps, xmaps, c, smem, stream)
-                   : launch_variant<2, false, false>(a, maps, xmaps, c, smem, stream);
+        if (gated) return f16 ? launch_variant<2, true, true>(a, blocks, maps, xmaps, c, smem, stream)
+                              : launch_variant<2, true, false>(a, blocks, maps, xmaps, c, smem, stream);
+        return f16 ? launch_variant<2, false, true>(a, blocks, maps, xmaps, c, smem, stream)
+                   : launch_variant<2, false, false>(a, blocks, maps, xmaps, c, smem, stream);
     }
-    if (gated) return f16 ? launch_variant<1, true, true>(a, maps, xmaps, c, smem, stream)
-                          : launch_variant<1, true, false>(a, maps, xmaps, c, smem, stream);
-    return f16 ? launch_variant<1, false, true>(a, maps, xmaps, c, smem, stream)
-               : launch_variant<1, false, false>(a, maps, xmaps, c, smem, stream);
+    if (gated) return f16 ? launch_variant<1, true, true>(a, blocks, maps, xmaps, c, smem, stream)
+                          : launch_variant<1, true, false>(a, blocks, maps, xmaps, c, smem, stream);
+    return f16 ? launch_variant<1, false, true>(a, blocks, maps, xmaps, c, smem, stream)
+               : launch_variant<1, false, false>(a, blocks, maps, xmaps, c, smem, stream);
 }
 
 }  // namespace dpa

@@ -409,6 +409,30 @@ def test_linear(rows, K, N, act, gated, bias, residual, dtype, out):
         assert torch.equal(h, y)
 
 
+@pytest.mark.parametrize("rows", [3, 16, 30, 70, 300, 2000])
+@pytest.mark.parametrize("K", [1024, 1096, 4096, 8192])
+def test_fp32_outputs_keep_their_accuracy_over_long_sums(rows, K):
+    # blocks of at most 256 inputs (17 steps of two roundings or truncations, 2^-23 of the block's
+    # magnitude each) are added with rounding, at most K / 32 + 16 times 2^-24 of the whole, with fewer
+    # blocks where few rows are summed in registers
+    g = gen(rows + K)
+    N = 2500 if rows > 200 else 96
+    ws = dpa.new_linear_workspace()
+    for dt in (torch.float16, torch.bfloat16):
+        x, w = normal(g, rows, K, dtype=dt), normal(g, N, K, dtype=dt, scale=K ** -0.5)
+        x[:, ::2] = x[:, ::2].abs()      # sums that grow: the accumulator is large for long
+        w[:, ::2] = w[:, ::2].abs()
+        mag = x.double().abs() @ w.double().abs().T
+        ref = x.double() @ w.double().T
+        tol = (34 * 2.0 ** -23 + (K / 32 + 16) * 2.0 ** -24) * mag
+        close(dpa.linear(x, w, ws, out_dtype=torch.float32), ref, tol)
+        if rows < 200:
+            off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device="cuda")
+            y = dpa.grouped_linear(x, off, torch.stack((w, w)), ws, out_dtype=torch.float32)
+            close(y, ref, tol)
+    assert dpa.device_status(ws) == 0
+
+
 # rows per group, K, N, act, gated, bias, residual
 GROUPED = [
     ([1], 64, 64, "none", False, False, False), ([0] * 70 + [40, 0, 3, 20] + [0] * 30, 1032, 90, "silu", True, True, True),
