@@ -39,6 +39,7 @@ CU_SOURCES = {
     "rates.cu": ["--fmad=false"],
     "pairs.cu": [],
     "linear_tc.cu": [],
+    "linear_tc_odd.cu": [],
     "linear_few.cu": [],
     "dense_abi.cu": [],
 }

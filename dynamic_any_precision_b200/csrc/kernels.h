@@ -265,7 +265,7 @@ struct UnpermuteBwdArgs {
 };
 cudaError_t launch_unpermute_bwd(const UnpermuteBwdArgs& a, int type, cudaStream_t stream, int sms);
 
-// Matrix products with a fused epilogue, plain or grouped by expert (linear_tc.cu).
+// Matrix products with a fused epilogue, plain or grouped by expert (linear_tc.cuh).
 struct LinearArgs {
     int rows, K, N;           // rows of x, in and out features
     int E;                    // groups (0: plain)
