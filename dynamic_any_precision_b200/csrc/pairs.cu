@@ -14,6 +14,7 @@
 #include <climits>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -538,6 +539,118 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamMaxCtas) unpermute_stre
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// The same for rows that are not whole 16-byte pieces: a row starts anywhere in a 16-byte block, so a
+// warp copies the aligned blocks that cover its run (the blocks' other elements are not used; behind
+// the end of the tensor nothing is read) and takes single elements from shared memory, lanes side by
+// side. (4096 tokens of 8 bf16 rows of 2047 and a residual take 91 us with loads of single
+// elements and 39 with this; 16384 tokens of 2: 203 and 63.)
+// Lanes are laid over whole 128-byte lines, so that a run asks for each of its lines once.
+constexpr int kShiftRow = kStreamPieces * 32 * 16 + 128;   // a warp's bytes of one row
+
+// Starts the copy of the 16-byte blocks that hold elements [at, at + n) of a tensor of `total` elements;
+// element `at` comes to place line_offset(at) of dst.
+template <typename T>
+__device__ __forceinline__ int line_offset(int64_t at) {
+    return static_cast<int>(at) & (128 / static_cast<int>(sizeof(T)) - 1);
+}
+template <int RUN, typename T>   // n <= RUN
+__device__ __forceinline__ void copy_blocks(uint32_t dst, const T* src, int64_t at, int n, int64_t total, int lane) {
+    constexpr int kPer = 16 / sizeof(T);
+    const int m = line_offset<T>(at), end = m + n;   // elements, from the line's start
+    const T* line = src + (at - m);
+    const int64_t rest = total - (at - m);   // elements from the line's start on; the last block may be short
+    const int left = rest < end + kPer ? static_cast<int>(rest) : end + kPer;
+#pragma unroll
+    for (int i = 0; i < (RUN / kPer + 31) / 32 + 1; ++i) {
+        const int e = (i * 32 + lane) * kPer;   // the block's first element
+        if (e + kPer > m && e < end)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + e * static_cast<int>(sizeof(T))), "l"(line + e),
+                         "r"(min(16, (left - e) * static_cast<int>(sizeof(T))))
+                         : "memory");
+    }
+}
+
+template <typename ZT, typename YT, typename RT>
+__global__ void __launch_bounds__(kStreamThreads, kStreamMaxCtas) unpermute_shift_kernel(UnpermuteArgs a, int runs,
+                                                                                         int stage_bytes) {
+    constexpr int kRun = kStreamPieces * 32 * (16 / sizeof(ZT)), kEach = kRun / 32;
+    extern __shared__ __align__(16) unsigned char ring[];
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t items = static_cast<int64_t>(a.T) * runs, warps = static_cast<int64_t>(gridDim.x) * (kStreamThreads / 32);
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * (kStreamThreads / 32) + (threadIdx.x >> 5);
+    const int64_t i0 = items * me / warps, i1 = items * (me + 1) / warps;   // items <= 2^30 * 2^24
+    if (i0 >= i1) return;
+    unsigned char* mine = ring + (threadIdx.x >> 5) * stage_bytes * kStreamStages;
+    const uint32_t base = smem_u32(mine);
+    const int64_t z_total = static_cast<int64_t>(a.T) * a.K * a.H, r_total = static_cast<int64_t>(a.T) * a.H;
+    Cursor in, out;
+    out.t = i0 / runs;
+    out.run = static_cast<int>(i0 - out.t * runs);
+    out.left = static_cast<int>(i1 - i0);
+    out.s0 = 0;
+    out.token(a, lane);
+    in = out;
+    auto issue = [&](int stage) {
+        if (in.left > 0) {
+            const int c = in.run * kRun, n = min(kRun, a.H - c);
+            const uint32_t dst = base + stage * stage_bytes;
+#pragma unroll
+            for (int u = 0; u < kStreamRows; ++u) {
+                if (in.s0 + u < in.n) {
+                    const unsigned p = __shfl_sync(0xffffffffu, in.s.p, (in.s0 + u) & 31);
+                    copy_blocks<kRun>(dst + u * kShiftRow, static_cast<const ZT*>(a.z), static_cast<int64_t>(p) * a.H + c,
+                                      n, z_total, lane);
+                }
+            }
+            if (a.residual && in.s0 + kStreamRows >= in.n)
+                copy_blocks<kRun>(dst + kStreamRows * kShiftRow, static_cast<const RT*>(a.residual), in.t * a.H + c, n,
+                                  r_total, lane);
+            in.advance(a, runs, lane);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < kStreamStages - 1; ++i) issue(i);
+    float acc[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) acc[j] = 0.f;
+    for (int stage = 0; out.left > 0; stage = stage + 1 == kStreamStages ? 0 : stage + 1) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStreamStages - 2) : "memory");
+        __syncwarp();   // every lane's copies are there, and every lane is done with the last round's stage
+        issue(stage == 0 ? kStreamStages - 1 : stage - 1);
+        const int c = out.run * kRun, n = a.H - c;
+        const unsigned char* src = mine + stage * stage_bytes;
+#pragma unroll
+        for (int u = 0; u < kStreamRows; ++u) {
+            if (out.s0 + u < out.n) {
+                const float w = __shfl_sync(0xffffffffu, out.s.w, (out.s0 + u) & 31);
+                const unsigned p = __shfl_sync(0xffffffffu, out.s.p, (out.s0 + u) & 31);
+                const ZT* z = reinterpret_cast<const ZT*>(src + u * kShiftRow) +
+                              line_offset<ZT>(static_cast<int64_t>(p) * a.H + c) + lane;
+#pragma unroll
+                for (int q = 0; q < kEach; q += 4) {
+                    if (32 * q < n) {   // elements behind the row are whatever the ring holds, and not stored
+#pragma unroll
+                        for (int j = q; j < q + 4; ++j) acc[j] = fmaf(w, up(z[32 * j]), acc[j]);
+                    }
+                }
+            }
+        }
+        if (out.s0 + kStreamRows >= out.n) {
+            YT* y = static_cast<YT*>(a.y) + out.t * a.H + c + lane;
+            const RT* r = reinterpret_cast<const RT*>(src + kStreamRows * kShiftRow) +
+                          line_offset<RT>(out.t * a.H + c) + lane;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                if (lane + 32 * j < n) y[32 * j] = down<YT>(a.residual ? up(r[32 * j]) + acc[j] : acc[j]);
+                acc[j] = 0.f;
+            }
+        }
+        out.advance(a, runs, lane);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Sums of 8 values over the lanes of a warp; lane l returns the sum of value l & 7 (in the order of
 // the butterfly, the same in every run): halves of the values are exchanged while there are several.
 __device__ __forceinline__ float warp_sums8(const float (&v)[8], int lane) {
@@ -562,14 +675,17 @@ __device__ __forceinline__ float warp_sums8(const float (&v)[8], int lane) {
     return c;
 }
 
-// `wpt` warps per token (8 / wpt tokens per CTA). Each thread reads its part of dy and the same part
-// of up to 8 slots' rows, writes the rows' gradients and adds to their dot products; the dot
-// products are then summed over the lanes and, in order, over the token's warps.
+// `wpt` warps per token (8 / wpt tokens per CTA), SLOTS rows at a time (2, 4 or 8), and more pieces of
+// them the fewer they are (16384 tokens of 2 rows of 2048 bf16 take 54 us, with 8 slots 71, with 2 and
+// one piece 62; of 2047 74, 143 and 91). Each thread
+// reads its part of dy and the same part of the slots' rows, writes the rows' gradients and adds to
+// their dot products; the dot products are then summed over the lanes and, in order, over the token's
+// warps.
 // Three CTAs per SM: two of them leave too few loads in flight (4096 tokens of 8 rows of 2048: fp32 109
 // against 93 us, bf16 50 against 49).
-template <typename T, int VEC>
+template <typename T, int VEC, int SLOTS>
 __global__ void __launch_bounds__(256, 3) unpermute_bwd_kernel(UnpermuteBwdArgs a, int wpt) {
-    constexpr int U = pieces(VEC);
+    constexpr int U = pieces(VEC) * (8 / SLOTS);
     __shared__ float s_dot[8][8];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wt = warp % wpt;
@@ -578,18 +694,17 @@ __global__ void __launch_bounds__(256, 3) unpermute_bwd_kernel(UnpermuteBwdArgs 
     Slots s{UINT_MAX, 0.f};
     if (live) s = load_slots(a.pos, a.weights, a.wtype, t, a.K, static_cast<unsigned>(a.T) * a.K, lane);
     const T* dyr = static_cast<const T*>(a.dy) + t * a.H;
-    for (int s0 = 0; s0 < a.K; s0 += 8) {
-        float dot[8], w[8];
-        unsigned p[8];
+    for (int s0 = 0; s0 < a.K; s0 += SLOTS) {
+        float dot[8] = {}, w[SLOTS];
+        unsigned p[SLOTS];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            dot[u] = 0.f;
+        for (int u = 0; u < SLOTS; ++u) {
             p[u] = __shfl_sync(0xffffffffu, s.p, (s0 + u) & 31);
             w[u] = __shfl_sync(0xffffffffu, s.w, (s0 + u) & 31);
             if (s0 + u >= a.K) p[u] = UINT_MAX;
         }
         for (int c0 = wt * (32 * VEC * U); live && c0 < a.H; c0 += wpt * (32 * VEC * U)) {
-            Pack<T, VEC> dy[U], z[8][U];
+            Pack<T, VEC> dy[U], z[SLOTS][U];
             int c[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
@@ -597,13 +712,13 @@ __global__ void __launch_bounds__(256, 3) unpermute_bwd_kernel(UnpermuteBwdArgs 
                 dy[i] = load_if<T, VEC>(dyr + c[i], c[i] < a.H);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < SLOTS; ++u) {
                 const T* zr = static_cast<const T*>(a.z) + static_cast<int64_t>(p[u] != UINT_MAX ? p[u] : 0u) * a.H;
 #pragma unroll
                 for (int i = 0; i < U; ++i) z[u][i] = load_if<T, VEC>(zr + c[i], p[u] != UINT_MAX && c[i] < a.H);
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < SLOTS; ++u) {
                 if (p[u] == UINT_MAX) continue;
                 T* dzr = static_cast<T*>(a.dz) + static_cast<int64_t>(p[u]) * a.H;
 #pragma unroll
@@ -630,14 +745,14 @@ __global__ void __launch_bounds__(256, 3) unpermute_bwd_kernel(UnpermuteBwdArgs 
             }
             __syncthreads();
         }
-        if (live && wt == 0 && lane < 8 && s0 + lane < a.K) a.dweights[t * a.K + s0 + lane] = d;
+        if (live && wt == 0 && lane < SLOTS && s0 + lane < a.K) a.dweights[t * a.K + s0 + lane] = d;
     }
 }
 
 // Warps per token: enough to fill the GPU (32 warps per SM), no more than the row has runs.
-int warps_per_token(int T, int H, int vec, int sms) {
+int warps_per_token(int T, int H, int run, int sms) {
     int w = 1;
-    while (w < 8 && static_cast<int64_t>(T) * w < 32 * sms && 32 * w * vec * pieces(vec) < H) w *= 2;
+    while (w < 8 && static_cast<int64_t>(T) * w < 32 * sms && w * run < H) w *= 2;
     return w;
 }
 
@@ -666,20 +781,27 @@ template <typename ZT, typename YT, typename RT>
 cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream, int sms) {
     constexpr int kWidest = sizeof(ZT) == 2 ? 8 : 4;
     const int vec = pack_of(a.H, kWidest);
-    int wpt = warps_per_token(a.T, a.H, vec, sms);
+    int wpt = warps_per_token(a.T, a.H, 32 * vec * pieces(vec), sms);
     UnpermuteArgs b = a;
     constexpr int kRun = kStreamPieces * 32 * kWidest;
     const int runs = (a.H - 1) / kRun + 1;
-    int stage_bytes = kStreamRes + (a.residual ? kStreamPieces * kStreamThreads * kWidest * static_cast<int>(sizeof(RT)) : 0);
-    const int smem = kStreamStages * stage_bytes;
+    const bool whole = vec == kWidest;
+    int stage_bytes = whole ? kStreamRes : kStreamRows * kShiftRow;   // shifted: of one warp
+    if (a.residual) stage_bytes += whole ? kRun * static_cast<int>(sizeof(RT)) * (kStreamThreads / 32)
+                                         : kRun * static_cast<int>(sizeof(RT)) + 128;
+    const int smem = kStreamStages * stage_bytes * (whole ? 1 : kStreamThreads / 32);
     int per_sm = kStreamSmem / (smem + 1024);   // the system takes 1 KB of each CTA's
     per_sm = per_sm < kStreamMaxCtas ? per_sm : kStreamMaxCtas;
     // two items per warp at least, and two CTAs per SM (8 rows of 2048 bf16 per token: at 512 tokens 5.5
     // us with the ring, 5.0 without; at 1024 tokens 8.0 and 13.2, at 4096 26.6 and 40.8)
-    const int64_t fed = static_cast<int64_t>(a.T) * runs / (kStreamThreads / 32 * 2);
-    if (vec == kWidest && fed >= 2 * sms) {
+    // Rows that start inside a block: full runs' worth of elements for four (8 rows per token; ring and
+    // without: 4096 tokens of 321 bf16 17.6 and 11.5, of 513 19.5 and 22.8; 16384 tokens of 65 fp32 27.8
+    // and 18.6, of 201 23.6 and 38.3).
+    const int64_t fed = (whole ? static_cast<int64_t>(a.T) * runs : static_cast<int64_t>(a.T) * a.H / kRun) / (kStreamThreads / 32 * 2);
+    if (fed >= (whole ? 2 : 4) * sms) {
         const int ctas = fed < per_sm * sms ? static_cast<int>(fed) : per_sm * sms;
-        const void* fn = reinterpret_cast<const void*>(unpermute_stream_kernel<ZT, YT, RT>);
+        const void* fn = whole ? reinterpret_cast<const void*>(unpermute_stream_kernel<ZT, YT, RT>)
+                               : reinterpret_cast<const void*>(unpermute_shift_kernel<ZT, YT, RT>);
         const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
         int r = runs;
@@ -704,13 +826,20 @@ template <typename T>
 cudaError_t unpermute_bwd_type(const UnpermuteBwdArgs& a, cudaStream_t stream, int sms) {
     constexpr int kWidest = 16 / sizeof(T);
     const int vec = pack_of(a.H, kWidest);
-    int wpt = warps_per_token(a.T, a.H, vec, sms);
+    const int slots = a.K <= 2 ? 2 : a.K <= 4 ? 4 : 8;
+    int wpt = warps_per_token(a.T, a.H, 32 * vec * pieces(vec) * (8 / slots), sms);
     UnpermuteBwdArgs b = a;
     void* args[] = {&b, &wpt};
-    const void* fn = vec == kWidest ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, kWidest>)
-                     : vec == 4     ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 4>)
-                     : vec == 2     ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 2>)
-                                    : reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 1>);
+    auto pick = [&](auto slots) {
+        constexpr int S = decltype(slots)::value;
+        return vec == kWidest ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, kWidest, S>)
+               : vec == 4     ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 4, S>)
+               : vec == 2     ? reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 2, S>)
+                              : reinterpret_cast<const void*>(unpermute_bwd_kernel<T, 1, S>);
+    };
+    const void* fn = slots == 2   ? pick(std::integral_constant<int, 2>{})
+                     : slots == 4 ? pick(std::integral_constant<int, 4>{})
+                                  : pick(std::integral_constant<int, 8>{});
     return launch_pdl_raw(fn, dim3((a.T - 1) / (8 / wpt) + 1), dim3(256), 0, stream, args);
 }
 

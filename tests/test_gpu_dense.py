@@ -171,6 +171,40 @@ def test_unpermute_rows(T, K, E, H, drop, types):
             close(y, ref, (K + 3) * 2.0 ** -24 * mag + rounding(ref, yt) * (1 + 2.0 ** -20))
 
 
+# batches long enough for the ring of copies, rows that start anywhere in a 16-byte block
+@pytest.mark.parametrize("types", ["bf16-bf16", "fp16-fp32", "fp32-fp32", "fp32-bf16"])
+@pytest.mark.parametrize("T,K,E,H,drop", [(2600, 2, 8, 65, 0.0), (5000, 3, 8, 1, 0.2), (2500, 8, 16, 331, 0.1), (900, 8, 16, 2047, 0.3),
+                                          (1200, 5, 16, 1036, 0.0), (2401, 32, 64, 70, 0.5)])
+def test_unpermute_rows_of_any_length(T, K, E, H, drop, types):
+    zt, yt = (DT[t] for t in types.split("-"))
+    _, pos, _, live = sorted_rows(T, K, E, drop, T + H)
+    g = gen(T * 3 + H)
+    z = normal(g, T * K, H, dtype=zt)
+    z[live:] = float("nan")
+    w = torch.rand((T, K), generator=g, device="cuda")
+    terms = torch.where((pos >= 0)[:, :, None], z[pos.clamp_min(0).long()].double(), 0.0) * w.double()[:, :, None]
+    for res in (None, normal(g, T, H, dtype=yt), normal(g, T, H)):
+        ref, mag = terms.sum(1), terms.abs().sum(1)
+        if res is not None:
+            ref, mag = ref + res.double(), mag + res.double().abs()
+        y = dpa.unpermute_rows(z, pos, w, residual=res, out_dtype=yt)
+        close(y, ref, (K + 3) * 2.0 ** -24 * mag + rounding(ref, yt) * (1 + 2.0 ** -20))
+        if res is not None and res.dtype == yt:    # in place
+            assert torch.equal(dpa.unpermute_rows(z, pos, w, residual=res, out=res), y)
+
+
+def test_unpermute_odd_rows_past_32_bit_offsets():
+    T, K, H = 65536, 8, 4101
+    pos = torch.randperm(T * K, generator=torch.Generator().manual_seed(3)).int().reshape(T, K).cuda()
+    pos[::2], pos[1] = pos[::2].flip(0).clone(), torch.arange(T * K - K, T * K, dtype=torch.int32, device="cuda")
+    z = normal(gen(2), T * K // 64, H, dtype=torch.bfloat16).repeat(64, 1)
+    y = dpa.unpermute_rows(z, pos)
+    tok = torch.tensor([0, 1, 32767, 65534, 65535], device="cuda")
+    terms = z[pos[tok].long()].double()
+    ref = terms.sum(1)
+    close(y[tok], ref, (K + 3) * 2.0 ** -24 * terms.abs().sum(1) + rounding(ref, torch.bfloat16) * (1 + 2.0 ** -20))
+
+
 def test_unpermute_rows_in_place_and_repeatable():
     T, K, H = 130, 8, 2048
     _, pos, _, _ = sorted_rows(T, K, 64, 0.0, 5)
