@@ -68,6 +68,26 @@ int split_k(int64_t tiles, int ksteps) {
     return 1;
 }
 
+// Rows per token tile, at most `most`, for pairs of CTAs: those for which the rounds of tiles over the
+// GPU's pairs take the least time, about rounds x (tile rows + 100).
+// Equal tiles of at most 256 alone leave pairs without work: 600x2048x4096 (48 tiles of 224 on 74 pairs)
+// 20.2 us, as 64 of 160 16.8; 2048x2048x1408 with a gate (two rounds of 256) 26.9, of 160 20.4;
+// 4819x1680x408 (one of 256) 21.8, of 160 17.0.
+int pair_rows(int rows, int most, int FT, int pairs) {
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int tn = most; tn > 0; tn -= 32) {   // a multiple of 16 per CTA
+        const int even = balanced_rows(rows, tn, 32);
+        const int64_t tiles = static_cast<int64_t>((rows - 1) / even + 1) * FT;
+        const int64_t cost = ((tiles - 1) / pairs + 1) * (even + 100);
+        if (cost < least) {
+            least = cost;
+            best = even;
+        }
+    }
+    return best;
+}
+
 // Whether the register kernel takes the call. Plain: up to 16 rows, and up to 32 where the weights are
 // small, so that start-up counts (32 rows: 2048x2816 6.6 us against 6.9 here; gated 10.4 against 8.3).
 // Grouped: up to 64 rows, 8 per group on average (8 tokens of top-8 through 128 experts of 2048x768
@@ -112,7 +132,7 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
         if (!pair) a.splits = split_k(tiles, a.ksteps);
         clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
     } else {
-        a.TN = balanced_rows(a.rows, !pair ? 128 : blocks ? kBlockedTokens : 256, 16 * CG);
+        a.TN = pair ? pair_rows(a.rows, blocks ? kBlockedTokens : 256, a.FT, sms / 2) : balanced_rows(a.rows, 128, 16);
         a.xbox = a.TN / CG;
         const int64_t tiles = static_cast<int64_t>((a.rows - 1) / a.TN + 1) * a.FT;
         if (tiles > INT32_MAX) return cudaErrorInvalidValue;
@@ -123,7 +143,7 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
     a.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // buffers are 16-byte aligned at least
     a.out_bytes = kOutBytes;
     if (a.splits > 1 && (a.TN + a.splits) * kRowsA * 4 > kOutBytes) a.out_bytes = (a.TN + a.splits) * kRowsA * 4;
-    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + a.out_bytes + kBarBytes + (a.E + 1) * 4;
+    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + a.out_bytes + kBarBytes + 2 * (a.E + 1) * 4;
     a.stages = (kSmemMax - fixed) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const size_t smem = static_cast<size_t>(a.stages) * stage + fixed;

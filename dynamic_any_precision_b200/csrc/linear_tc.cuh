@@ -78,19 +78,22 @@ struct Tile {
     int e, row0, n, ft;
 };
 
-// Rows of one token tile when n rows are cut into tiles of at most tn: equal parts rounded up to
-// `step` rows.
-__host__ __device__ __forceinline__ int balanced_rows(int n, int tn, int step) {
-    const int nt = (n + tn - 1) / tn;
-    return nt == 0 ? step : ((n + nt - 1) / nt + step - 1) / step * step;
+// Rows of one token tile when n rows are cut into nt tiles: equal parts rounded up to `step` rows. With
+// tiles of at most tn rows, a multiple of step, nt is n / tn rounded up, and so is n / the result.
+__host__ __device__ __forceinline__ int tile_rows(int n, int nt, int step) {
+    const int each = nt == 1 ? n : (n - 1) / nt + 1;
+    return (each + step - 1) / step * step;
 }
+__host__ __device__ __forceinline__ int balanced_rows(int n, int tn, int step) { return tile_rows(n, (n - 1) / tn + 1, step); }
 
 __device__ __forceinline__ int group_edge(const LinearArgs& a, int e) {
     return min(max(__ldg(a.offsets + e), 0), a.rows);   // an edge outside the rows reads as the nearest row
 }
 
+// Called by whole warps. s_pref: token tiles before each group, s_off: the groups' edges. The group is
+// the last one whose first tile is not after the tile: found 32 groups at a time, then among 32.
 template <int CG>
-__device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref, int tile) {
+__device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref, const int* s_off, int tile, int lane) {
     Tile t;
     int tt = static_cast<int>(static_cast<unsigned>(tile) / static_cast<unsigned>(a.FT));
     t.ft = tile - tt * a.FT;
@@ -100,16 +103,14 @@ __device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref
         t.n = min(a.rows - t.row0, a.TN);
         return t;
     }
-    int lo = 0, hi = a.E - 1;   // the last group whose first token tile is not after tt
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_pref[mid] <= tt) lo = mid;
-        else hi = mid - 1;
-    }
-    t.e = lo;
-    tt -= s_pref[lo];
-    const int begin = group_edge(a, lo), n = group_edge(a, lo + 1) - begin;
-    const int sz = balanced_rows(n, a.TN, 16 * CG);
+    int e = 32 * lane;   // E <= 1024
+    const int block = 32 * (__popc(__ballot_sync(0xffffffffu, e < a.E && s_pref[e] <= tt)) - 1);
+    e = block + lane;
+    e = block + __popc(__ballot_sync(0xffffffffu, e < a.E && s_pref[e] <= tt)) - 1;
+    const int first = s_pref[e], nt = s_pref[e + 1] - first, begin = s_off[e], n = s_off[e + 1] - begin;
+    const int sz = tile_rows(n, nt, 16 * CG);
+    tt -= first;
+    t.e = e;
     t.row0 = begin + tt * sz;
     t.n = min(n - tt * sz, sz);
     return t;
@@ -290,28 +291,36 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// Eight biases of one group's features (zeros without a bias and behind the last feature).
-template <bool F16, bool VEC>
-__device__ __forceinline__ void load_bias(const void* b, int64_t at, int cnt, int fs, Two (&out)[4]) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+// Eight biases of one group's features (zeros without a bias and behind the last feature), as loaded:
+// turned into fp32 by biases() after the wait for the sums.
+struct Bias8 {
+    uint32_t w[4];
+};
+template <bool VEC>
+__device__ __forceinline__ Bias8 load_bias(const void* b, int64_t at, int cnt, int fs) {
+    Bias8 r = {};
     if (b && cnt > 0) {
         const uint16_t* p = static_cast<const uint16_t*>(b) + at;
         if (VEC) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-            w[0] = v.x;
-            w[1] = v.y;
-            w[2] = v.z;
-            w[3] = v.w;
+            r.w[0] = v.x;
+            r.w[1] = v.y;
+            r.w[2] = v.z;
+            r.w[3] = v.w;
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[i] = (2 * i < cnt ? __ldg(p + 2 * i * fs) : 0u) |
-                       (2 * i + 1 < cnt ? static_cast<uint32_t>(__ldg(p + (2 * i + 1) * fs)) << 16 : 0u);
+                r.w[i] = (2 * i < cnt ? __ldg(p + 2 * i * fs) : 0u) |
+                         (2 * i + 1 < cnt ? static_cast<uint32_t>(__ldg(p + (2 * i + 1) * fs)) << 16 : 0u);
         }
     }
+    return r;
+}
+template <bool F16>
+__device__ __forceinline__ void biases(const Bias8& b, Two (&out)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        out[i] = two(up16<F16>(static_cast<uint16_t>(w[i])), up16<F16>(static_cast<uint16_t>(w[i] >> 16)));
+        out[i] = two(up16<F16>(static_cast<uint16_t>(b.w[i])), up16<F16>(static_cast<uint16_t>(b.w[i] >> 16)));
 }
 
 // Bias, activation and gate of eight sums (g; m: the second product's).
@@ -374,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(done + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     int* s_pref = reinterpret_cast<int*>(tail + kBarBytes);   // [E + 1] token tiles before each group
+    int* s_off = s_pref + a.E + 1;                            // [E + 1] first row of each group
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.splits;                                     // CTAs sharing K (CG = 1)
@@ -416,28 +426,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         }
     }
     pdl_wait();
-    // token tiles before each group (one warp; the others wait at the barrier below)
-    if (a.E > 0 && warp == kLoadWarp) {
-        int before = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            int c = 0;
-            if (e < a.E) {
-                const int n = group_edge(a, e + 1) - group_edge(a, e);
-                if (n > 0) {
-                    const int sz = balanced_rows(n, a.TN, 16 * CG);
-                    c = (n + sz - 1) / sz;
-                }
-            }
-            int incl = c;
+    // edges of the groups and token tiles before each: counted by all threads, added up by one warp
+    if (a.E > 0) {
+        for (int e = tid; e <= a.E; e += kThreads) {
+            const int begin = group_edge(a, e), n = e < a.E ? group_edge(a, e + 1) - begin : 0;
+            s_off[e] = begin;
+            s_pref[e] = n > 0 ? (n - 1) / a.TN + 1 : 0;
+        }
+        __syncthreads();
+        if (warp == kLoadWarp) {
+            const int each = a.E / 32 + 1, e0 = min(lane * each, a.E + 1), e1 = min(e0 + each, a.E + 1);
+            int sum = 0;
+            for (int e = e0; e < e1; ++e) sum += s_pref[e];
+            int incl = sum;
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            if (e < a.E) s_pref[e] = before + incl - c;
-            before += __shfl_sync(0xffffffffu, incl, 31);
+            int before = incl - sum;
+            for (int e = e0; e < e1; ++e) {
+                const int c = s_pref[e];
+                s_pref[e] = before;
+                before += c;
+            }
         }
-        if (lane == 0) s_pref[a.E] = before;
     }
     tc_fence_before();
     __syncthreads();
@@ -460,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             int s = 0, ph = 1;
             bool ok = true;
             for (int it = cid; it < ntiles && ok; it += ncl) {
-                const Tile t = find_tile<CG>(a, s_pref, it);
+                const Tile t = find_tile<CG>(a, s_pref, s_off, it, lane);
                 const int part = ((t.n + 16 * CG - 1) / (16 * CG)) * 16;   // token rows of this CTA
                 int mi = 0, box = a.xbox;
                 while (box < part) {   // grouped only: a plain tile's box holds it
@@ -505,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             int s = 0, ph = 0, j = 0;   // j: accumulators filled
             bool ok = true;
             for (int it = cid; it < ntiles && ok; it += ncl) {
-                const Tile t = find_tile<CG>(a, s_pref, it);
+                const Tile t = find_tile<CG>(a, s_pref, s_off, it, lane);
                 const int ncols = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
                 const uint32_t idesc = instr_desc(F16 ? 0 : 1, ncols, 128 * CG);
                 for (int kb = k0, kend; kb < k1 && ok; kb = kend, ++j) {
@@ -580,16 +592,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         const uint32_t sums = tmem + lane_base + static_cast<uint32_t>(2 * kAccCols);   // of a tile's K blocks
         int j = 0;
         for (int it = cid; it < ntiles; it += ncl, ++j) {
-            const Tile t = find_tile<CG>(a, s_pref, it);
+            const Tile t = find_tile<CG>(a, s_pref, s_off, it, lane);
             const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + (VEC ? fg * 8 : fg);
             const int cnt = min(max((a.N - f + fs - 1) / fs, 0), 8);
             const int nch = (t.n + kChunk - 1) / kChunk;
-            Two bias[4], bmul[4];
+            Bias8 bias_raw = {}, bmul_raw = {};
             Out8 res[kItems];
             if (CG == 2 || S == 1) {   // operands of the epilogue: loaded while the MMAs run
                 const int64_t fb = static_cast<int64_t>(t.e) * a.N + f;
-                load_bias<F16, VEC>(a.bias, fb, cnt, fs, bias);
-                if (GATED) load_bias<F16, VEC>(a.bias_mul, fb, cnt, fs, bmul);
+                bias_raw = load_bias<VEC>(a.bias, fb, cnt, fs);
+                if (GATED) bmul_raw = load_bias<VEC>(a.bias_mul, fb, cnt, fs);
                 if (a.residual && cnt > 0) {
 #pragma unroll
                     for (int i = 0; i < kItems; ++i) {
@@ -660,6 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                 }
                 break;   // one tile per cluster
             }
+            Two bias[4], bmul[4];
+            biases<F16>(bias_raw, bias);
+            if (GATED) biases<F16>(bmul_raw, bmul);
             for (int c = grp; c < nch; c += kGroups) {
                 uint32_t v[kChunk];
                 read_sums(c, v);
@@ -704,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         __syncwarp();
         cluster_sync();                          // every partial sum has arrived
         if (cid < ntiles) {
-            const Tile t = find_tile<CG>(a, s_pref, cid);
+            const Tile t = find_tile<CG>(a, s_pref, s_off, cid, lane);
             const int slice = (t.n + S - 1) / S * kRowsA, mine = (t.n - rank + S - 1) / S;
             constexpr int kFeatGroups = kFeat / 8, fs = VEC ? 1 : kFeatGroups;
             for (int i = tid; i < mine * kFeatGroups; i += kThreads) {
@@ -715,8 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                 const int64_t at = (static_cast<int64_t>(t.row0) + place * S + rank) * a.N + f;
                 Two bias[4], bmul[4], g[4], m[4];
                 Out8 res;
-                load_bias<F16, VEC>(a.bias, fb, cnt, fs, bias);
-                if (GATED) load_bias<F16, VEC>(a.bias_mul, fb, cnt, fs, bmul);
+                biases<F16>(load_bias<VEC>(a.bias, fb, cnt, fs), bias);
+                if (GATED) biases<F16>(load_bias<VEC>(a.bias_mul, fb, cnt, fs), bmul);
                 if (a.residual) res = load_residual<VEC>(a, at, cnt, fs);
                 const float* src = s_out + place * kRowsA;
                 auto sums = [&](int col, Two (&v)[4]) {
