@@ -278,12 +278,13 @@ struct LinearArgs {
     WsHeader* hdr;
     // set by the launcher: K steps, feature tiles, most tokens per tile, CTAs sharing K, pipeline
     // stages, rows of the smallest token load, tiles (plain), bytes of the epilogue's shared memory,
-    // whether out is 32-byte aligned
-    int ksteps, FT, TN, splits, stages, xbox, ntiles, out_bytes, out_wide;
+    // whether out is 32-byte aligned, and how far a cluster's next tile lies (token tiles, then
+    // feature tiles)
+    int ksteps, FT, TN, splits, stages, xbox, ntiles, out_bytes, out_wide, step_t, step_f;
 };
 cudaError_t launch_linear(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
                           cudaStream_t stream, int sms);
-// The products of few rows (linear_few.cu): at most 32 plain ones, or any that lie in few per group.
+// The products of few rows (linear_few.cu): at most 32 plain ones, or 64 that lie in few per group.
 cudaError_t launch_linear_few(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
                               cudaStream_t stream, int sms);
 

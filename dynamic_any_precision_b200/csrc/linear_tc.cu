@@ -140,10 +140,12 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
         if (!pair) a.splits = split_k(tiles, a.ksteps);
         clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
     }
+    a.step_t = static_cast<int>(clusters) / a.FT;
+    a.step_f = static_cast<int>(clusters) % a.FT;
     a.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // buffers are 16-byte aligned at least
     a.out_bytes = kOutBytes;
     if (a.splits > 1 && (a.TN + a.splits) * kRowsA * 4 > kOutBytes) a.out_bytes = (a.TN + a.splits) * kRowsA * 4;
-    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + a.out_bytes + kBarBytes + 2 * (a.E + 1) * 4;
+    const int stage = kATile + a.TN / CG * 128, fixed = 1024 + a.out_bytes + kBarBytes + 3 * (a.E + 1) * 4;
     a.stages = (kSmemMax - fixed) / stage;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     const size_t smem = static_cast<size_t>(a.stages) * stage + fixed;

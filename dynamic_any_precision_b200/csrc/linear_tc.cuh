@@ -90,31 +90,50 @@ __device__ __forceinline__ int group_edge(const LinearArgs& a, int e) {
     return min(max(__ldg(a.offsets + e), 0), a.rows);   // an edge outside the rows reads as the nearest row
 }
 
-// Called by whole warps. s_pref: token tiles before each group, s_off: the groups' edges. The group is
-// the last one whose first tile is not after the tile: found 32 groups at a time, then among 32.
-template <int CG>
-__device__ __forceinline__ Tile find_tile(const LinearArgs& a, const int* s_pref, const int* s_off, int tile, int lane) {
-    Tile t;
-    int tt = static_cast<int>(static_cast<unsigned>(tile) / static_cast<unsigned>(a.FT));
-    t.ft = tile - tt * a.FT;
-    t.e = 0;
-    if (a.E == 0) {   // plain: the launcher's TN is the tiles' size
-        t.row0 = tt * a.TN;
-        t.n = min(a.rows - t.row0, a.TN);
+// Groups' tables in shared memory (grouped): token tiles before each group and its first row, [E + 1]
+// each, and the rows of its tiles, [E].
+struct GroupTables {
+    int *pref, *off, *rows;
+};
+
+// A warp's way through its cluster's tiles, every ncl-th one from `cid` on, features innermost.
+// Divisions are left out of it: with few K steps a tile takes little longer than finding it did (128
+// experts, 12 steps: 97 to 114 us with a division and a search through all groups per tile, 95 to 100 without).
+struct TileCursor {
+    int tt, ft, e;   // token tile, feature tile, group (of an earlier tile until find)
+
+    __device__ __forceinline__ TileCursor(const LinearArgs& a, int cid)
+        : tt(static_cast<int>(static_cast<unsigned>(cid) / static_cast<unsigned>(a.FT))), ft(cid - tt * a.FT), e(0) {}
+    __device__ __forceinline__ void advance(const LinearArgs& a) {
+        tt += a.step_t;
+        ft += a.step_f;
+        if (ft >= a.FT) {
+            ft -= a.FT;
+            ++tt;
+        }
+    }
+    // Called by whole warps: the group is the last one whose first tile is not after the tile.
+    __device__ __forceinline__ Tile find(const LinearArgs& a, const GroupTables& g, int lane) {
+        Tile t;
+        t.ft = ft;
+        t.e = 0;
+        if (a.E == 0) {   // plain: the launcher's TN is the tiles' size
+            t.row0 = tt * a.TN;
+            t.n = min(a.rows - t.row0, a.TN);
+            return t;
+        }
+        for (int c = 32; c == 32;) {
+            const int x = e + lane;
+            c = __popc(__ballot_sync(0xffffffffu, x < a.E && g.pref[x] <= tt));   // at least one
+            e += c - 1;
+        }
+        const int begin = g.off[e], n = g.off[e + 1] - begin, sz = g.rows[e], skip = (tt - g.pref[e]) * sz;
+        t.e = e;
+        t.row0 = begin + skip;
+        t.n = min(n - skip, sz);
         return t;
     }
-    int e = 32 * lane;   // E <= 1024
-    const int block = 32 * (__popc(__ballot_sync(0xffffffffu, e < a.E && s_pref[e] <= tt)) - 1);
-    e = block + lane;
-    e = block + __popc(__ballot_sync(0xffffffffu, e < a.E && s_pref[e] <= tt)) - 1;
-    const int first = s_pref[e], nt = s_pref[e + 1] - first, begin = s_off[e], n = s_off[e + 1] - begin;
-    const int sz = tile_rows(n, nt, 16 * CG);
-    tt -= first;
-    t.e = e;
-    t.row0 = begin + tt * sz;
-    t.n = min(n - tt * sz, sz);
-    return t;
-}
+};
 
 // Eight outputs (or residual values) of one token. VEC (N % 8 == 0): consecutive features, 16-byte
 // aligned and wholly inside or outside N. Otherwise the first `cnt` of features `fs` apart, fs lanes
@@ -382,8 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     uint64_t* done = acc_empty + 2;
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(done + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-    int* s_pref = reinterpret_cast<int*>(tail + kBarBytes);   // [E + 1] token tiles before each group
-    int* s_off = s_pref + a.E + 1;                            // [E + 1] first row of each group
+    GroupTables groups;
+    groups.pref = reinterpret_cast<int*>(tail + kBarBytes);
+    groups.off = groups.pref + a.E + 1;
+    groups.rows = groups.off + a.E + 1;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.splits;                                     // CTAs sharing K (CG = 1)
@@ -430,14 +451,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     if (a.E > 0) {
         for (int e = tid; e <= a.E; e += kThreads) {
             const int begin = group_edge(a, e), n = e < a.E ? group_edge(a, e + 1) - begin : 0;
-            s_off[e] = begin;
-            s_pref[e] = n > 0 ? (n - 1) / a.TN + 1 : 0;
+            const int nt = n > 0 ? (n - 1) / a.TN + 1 : 0;
+            groups.off[e] = begin;
+            groups.pref[e] = nt;
+            if (e < a.E) groups.rows[e] = nt > 0 ? tile_rows(n, nt, 16 * CG) : 0;
         }
         __syncthreads();
         if (warp == kLoadWarp) {
             const int each = a.E / 32 + 1, e0 = min(lane * each, a.E + 1), e1 = min(e0 + each, a.E + 1);
             int sum = 0;
-            for (int e = e0; e < e1; ++e) sum += s_pref[e];
+            for (int e = e0; e < e1; ++e) sum += groups.pref[e];
             int incl = sum;
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -445,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             }
             int before = incl - sum;
             for (int e = e0; e < e1; ++e) {
-                const int c = s_pref[e];
-                s_pref[e] = before;
+                const int c = groups.pref[e];
+                groups.pref[e] = before;
                 before += c;
             }
         }
@@ -456,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     if constexpr (CG == 2) cluster_sync();   // the pair's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    int ntiles = a.E > 0 ? s_pref[a.E] * a.FT : a.ntiles;
+    int ntiles = a.E > 0 ? groups.pref[a.E] * a.FT : a.ntiles;
     if (S > 1 && ntiles > ncl) ntiles = ncl;   // one tile per cluster (only offsets out of order name more)
     // this CTA's K steps
     const int k0 = CG == 1 ? a.ksteps * rank / S : 0, k1 = CG == 1 ? a.ksteps * (rank + 1) / S : a.ksteps;
@@ -471,8 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
             int s = 0, ph = 1;
             bool ok = true;
-            for (int it = cid; it < ntiles && ok; it += ncl) {
-                const Tile t = find_tile<CG>(a, s_pref, s_off, it, lane);
+            TileCursor cursor(a, cid);
+            for (int it = cid; it < ntiles && ok; it += ncl, cursor.advance(a)) {
+                const Tile t = cursor.find(a, groups, lane);
                 const int part = ((t.n + 16 * CG - 1) / (16 * CG)) * 16;   // token rows of this CTA
                 int mi = 0, box = a.xbox;
                 while (box < part) {   // grouped only: a plain tile's box holds it
@@ -516,8 +540,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
             const uint64_t dconst = smem_desc_sw128(0);
             int s = 0, ph = 0, j = 0;   // j: accumulators filled
             bool ok = true;
-            for (int it = cid; it < ntiles && ok; it += ncl) {
-                const Tile t = find_tile<CG>(a, s_pref, s_off, it, lane);
+            TileCursor cursor(a, cid);
+            for (int it = cid; it < ntiles && ok; it += ncl, cursor.advance(a)) {
+                const Tile t = cursor.find(a, groups, lane);
                 const int ncols = (t.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
                 const uint32_t idesc = instr_desc(F16 ? 0 : 1, ncols, 128 * CG);
                 for (int kb = k0, kend; kb < k1 && ok; kb = kend, ++j) {
@@ -591,8 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         const bool blocked = BLOCKED && k1 - k0 > kBlockedSteps;
         const uint32_t sums = tmem + lane_base + static_cast<uint32_t>(2 * kAccCols);   // of a tile's K blocks
         int j = 0;
-        for (int it = cid; it < ntiles; it += ncl, ++j) {
-            const Tile t = find_tile<CG>(a, s_pref, s_off, it, lane);
+        TileCursor cursor(a, cid);
+        for (int it = cid; it < ntiles; it += ncl, ++j, cursor.advance(a)) {
+            const Tile t = cursor.find(a, groups, lane);
             const int f = (t.ft * CG + (CG == 2 ? rank : 0)) * kFeat + (VEC ? fg * 8 : fg);
             const int cnt = min(max((a.N - f + fs - 1) / fs, 0), 8);
             const int nch = (t.n + kChunk - 1) / kChunk;
@@ -719,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         __syncwarp();
         cluster_sync();                          // every partial sum has arrived
         if (cid < ntiles) {
-            const Tile t = find_tile<CG>(a, s_pref, s_off, cid, lane);
+            const Tile t = TileCursor(a, cid).find(a, groups, lane);
             const int slice = (t.n + S - 1) / S * kRowsA, mine = (t.n - rank + S - 1) / S;
             constexpr int kFeatGroups = kFeat / 8, fs = VEC ? 1 : kFeatGroups;
             for (int i = tid; i < mine * kFeatGroups; i += kThreads) {
