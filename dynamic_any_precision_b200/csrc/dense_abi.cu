@@ -1,5 +1,6 @@
 // C ABI of the expert row sort and of the dense matrix products (include/dpa.h): validation and
 // launches.
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -33,9 +34,15 @@ bool check_weights(const void* w, int wtype) {
     return !w || (aligned16(w) && (wtype == DPA_DTYPE_FP32 || wtype == DPA_DTYPE_FP64));
 }
 
+// SMs of the current device, asked once per device
 int sms_current() {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
     int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return n;
+    if (dev < kDevices && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && dev < kDevices)
+        known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -413,6 +413,20 @@ def _arg(t, name: str, shape, code, dev: int) -> int:
     raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+def _own(t, name: str) -> int:
+    """Pointer of the tensor that the call's sizes, type and device are taken from, or that the call
+    has made itself."""
+    if t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _workspace(ws, dev: int) -> int:
+    if _DTYPES.get(ws.dtype) == "uint8" and ws.get_device() == dev and ws.is_contiguous():
+        return ws.data_ptr()
+    return _arg(ws, "ws", ws.shape, "uint8", dev)   # names what is wrong
+
+
 def _call(fn, where: str, dev: int, stream, *args):
     """Run a device call on `dev`, on the given stream or that device's current one."""
     raw = _raw_stream(dev) if stream is None else stream.cuda_stream
@@ -471,15 +485,23 @@ def sort_pairs(idx, n_experts: int, ws, pos=None, order=None, offsets=None, stre
     [n_experts + 1]), int32: the place of each pair (-1 if not routed), the pair at each place
     (unrouted ones last), the places before each expert."""
     dev, P = _device(idx), idx.numel()
+    ip = _arg(idx, "idx", idx.shape, "int32", dev)
     if pos is None:
         pos = _like(idx, stream)
+        pp = pos.data_ptr()
+    else:
+        pp = _arg(pos, "pos", idx.shape, "int32", dev)
     if order is None:
         order = _new(idx, P, idx.dtype, stream)
+        op = order.data_ptr()
+    else:
+        op = _arg(order, "order", (P,), "int32", dev)
     if offsets is None:
         offsets = _new(idx, n_experts + 1, idx.dtype, stream)
-    _call(lib().dpa_sort_pairs, "dpa_sort_pairs", dev, stream, _arg(idx, "idx", idx.shape, "int32", dev), P, n_experts,
-          _arg(pos, "pos", idx.shape, "int32", dev), _arg(order, "order", (P,), "int32", dev),
-          _arg(offsets, "offsets", (n_experts + 1,), "int32", dev), _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
+        fp = offsets.data_ptr()
+    else:
+        fp = _arg(offsets, "offsets", (n_experts + 1,), "int32", dev)
+    _call(lib().dpa_sort_pairs, "dpa_sort_pairs", dev, stream, ip, P, n_experts, pp, op, fp, _workspace(ws, dev), ws.numel())
     return pos, order, offsets
 
 
@@ -489,10 +511,13 @@ def permute_rows(x, pos, out=None, stream=None):
     uninitialised)."""
     dev, code = _device(x), _float_type(x)
     (T, H), K = x.shape, pos.shape[-1]
+    xp, pp = _own(x, "x"), _arg(pos, "pos", (T, K), "int32", dev)
     if out is None:
         out = _new(x, (T * K, H), x.dtype, stream)
-    _call(lib().dpa_permute_rows, "dpa_permute_rows", dev, stream, code, _arg(x, "x", x.shape, code, dev),
-          _arg(pos, "pos", (T, K), "int32", dev), T, K, H, _arg(out, "out", (T * K, H), code, dev))
+        yp = out.data_ptr()
+    else:
+        yp = _arg(out, "out", (T * K, H), code, dev)
+    _call(lib().dpa_permute_rows, "dpa_permute_rows", dev, stream, code, xp, pp, T, K, H, yp)
     return out
 
 
@@ -518,14 +543,14 @@ def unpermute_rows(z, pos, weights=None, residual=None, out=None, out_dtype=None
     weights: fp32 or fp64 [T][K] (None: all 1); residual: [T][H] of y's type or fp32, may be `out`.
     y has out_dtype (default: residual's, else z's): z's own type, or one of the two is fp32."""
     dev, (T, K), H = _device(z), pos.shape, z.shape[-1]
-    out = _out(out, (T, H), z, residual, out_dtype, stream)
+    given, out = out is not None, _out(out, (T, H), z, residual, out_dtype, stream)
     code, zcode, wcode = _float_type(out), _float_type(z), _real(weights)
     rcode = code if residual is None else _float_type(residual)
     _call(lib().dpa_unpermute_rows, "dpa_unpermute_rows", dev, stream, zcode,
           _arg(z, "z", (T * K, H), zcode, dev), _arg(pos, "pos", (T, K), "int32", dev),
           None if weights is None else _arg(weights, "weights", (T, K), wcode, dev), wcode,
           None if residual is None else _arg(residual, "residual", (T, H), rcode, dev), rcode, code, T, K, H,
-          _arg(out, "out", (T, H), code, dev))
+          _arg(out, "out", (T, H), code, dev) if given else out.data_ptr())
     return out
 
 
@@ -547,15 +572,22 @@ def unpermute_rows_backward(dy, z, pos, weights, dz=None, dweights=None, stream=
     code, wcode = _float_type(z), _real(weights)
     if weights is None:
         raise ValueError("weights: expected a tensor")
+    zp = _arg(z, "z", (T * K, H), code, dev)
     if dz is None:
         dz = _like(z, stream)
+        dzp = dz.data_ptr()
+    else:
+        dzp = _arg(dz, "dz", (T * K, H), code, dev)
     if dweights is None:
         import torch
         dweights = _new(z, (T, K), torch.float32, stream)
+        dwp = dweights.data_ptr()
+    else:
+        dwp = _arg(dweights, "dweights", (T, K), DTYPE_FP32, dev)
     _call(lib().dpa_unpermute_rows_backward, "dpa_unpermute_rows_backward", dev, stream, code,
-          _arg(dy, "dy", (T, H), code, dev), _arg(z, "z", (T * K, H), code, dev),
+          _arg(dy, "dy", (T, H), code, dev), zp,
           _arg(pos, "pos", (T, K), "int32", dev), _arg(weights, "weights", (T, K), wcode, dev), wcode, T, K, H,
-          _arg(dz, "dz", (T * K, H), code, dev), _arg(dweights, "dweights", (T, K), DTYPE_FP32, dev))
+          dzp, dwp)
     return dz, dweights
 
 
@@ -563,13 +595,13 @@ def _product(fn, where, x, w, lead, groups, ws, bias, act, w_mul, bias_mul, resi
     """linear and grouped_linear: `lead` is () or (n_groups,), `groups` the group arguments of the
     call: () or (n_groups, offsets)."""
     dev, (rows, K), N = _device(x), x.shape, w.shape[-2]
-    out = _out(out, (rows, N), x, residual, out_dtype, stream)
+    wide, flat, rect = lead + (N, K), lead + (N,), (rows, N)
+    given, out = out is not None, _out(out, rect, x, residual, out_dtype, stream)
     code, ocode = _float_type(x), _float_type(out)
     rcode = ocode if residual is None else _float_type(residual)
-    wide, flat, rect = lead + (N, K), lead + (N,), (rows, N)
     if act not in ACTS:
         raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
-    xp = _arg(x, "x", x.shape, code, dev)
+    xp = _own(x, "x")
     if groups:
         groups = (groups[0], xp, _arg(groups[1], "offsets", (groups[0] + 1,), "int32", dev))
     else:
@@ -579,7 +611,7 @@ def _product(fn, where, x, w, lead, groups, ws, bias, act, w_mul, bias_mul, resi
           None if w_mul is None else _arg(w_mul, "w_mul", wide, code, dev),
           None if bias_mul is None else _arg(bias_mul, "bias_mul", flat, code, dev),
           None if residual is None else _arg(residual, "residual", rect, rcode, dev),
-          _arg(out, "out", rect, ocode, dev), _arg(ws, "ws", ws.shape, "uint8", dev), ws.numel())
+          _arg(out, "out", rect, ocode, dev) if given else out.data_ptr(), _workspace(ws, dev), ws.numel())
     return out
 
 
