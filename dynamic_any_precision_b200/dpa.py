@@ -367,19 +367,19 @@ def residual_rmsnorm(h, x, y=None, stream=None):
 # ------------------------------------------------------------- dense experts: rows and products
 
 _DTYPES = _FLOATS = None
-_current_device = _raw_stream = _empty_like = None
+_current_device = _raw_stream = _empty_like = _empty_strided = None
 
 
 def _torch_tables():
     """Element types and the current device and stream, looked up once (torch is imported late).
     int16 and uint16 tensors hold bf16 bit patterns."""
-    global _DTYPES, _FLOATS, _current_device, _raw_stream, _empty_like
+    global _DTYPES, _FLOATS, _current_device, _raw_stream, _empty_like, _empty_strided
     import torch
     _FLOATS = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.uint16: DTYPE_BF16,
                torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32, torch.float64: DTYPE_FP64}
     _DTYPES = {**_FLOATS, torch.int32: "int32", torch.uint8: "uint8"}
     _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _empty_like = torch.empty_like
+    _empty_like, _empty_strided = torch.empty_like, torch.empty_strided
 
 
 def _device(t) -> int:
@@ -441,12 +441,15 @@ def _call(fn, where: str, dev: int, stream, *args):
 
 
 def _new(like, shape, dtype, stream):
-    """A new tensor on `like`'s device, taken from the memory of the stream that the call runs on."""
+    """A new tensor on `like`'s device, taken from the memory of the stream that the call runs on.
+    shape: (n,) or (n, m), with its strides given (empty_strided takes 1.4 us of host time, new_empty
+    2.2 to 3.5)."""
+    strides = (1,) if len(shape) == 1 else (shape[1], 1)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _empty_strided(shape, strides, dtype=dtype, device=like.device)
     import torch
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return _empty_strided(shape, strides, dtype=dtype, device=like.device)
 
 
 def _like(t, stream):
@@ -492,12 +495,12 @@ def sort_pairs(idx, n_experts: int, ws, pos=None, order=None, offsets=None, stre
     else:
         pp = _arg(pos, "pos", idx.shape, "int32", dev)
     if order is None:
-        order = _new(idx, P, idx.dtype, stream)
+        order = _new(idx, (P,), idx.dtype, stream)
         op = order.data_ptr()
     else:
         op = _arg(order, "order", (P,), "int32", dev)
     if offsets is None:
-        offsets = _new(idx, n_experts + 1, idx.dtype, stream)
+        offsets = _new(idx, (n_experts + 1,), idx.dtype, stream)
         fp = offsets.data_ptr()
     else:
         fp = _arg(offsets, "offsets", (n_experts + 1,), "int32", dev)
