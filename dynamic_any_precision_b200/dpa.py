@@ -569,7 +569,7 @@ def _real(weights) -> int:
 
 def unpermute_rows_backward(dy, z, pos, weights, dz=None, dweights=None, stream=None):
     """Gradients of unpermute_rows: (dz [T*K][H] in z's type, dweights fp32 [T][K]). dy: [T][H] of
-    z's type. Rows of dz that no pair takes are left as they were (with dz=None: uninitialised);
+    z's type; dz may be z. Rows of dz that no pair takes are left as they were (with dz=None: uninitialised);
     pairs that are not routed get dweights 0. The residual's gradient is dy itself."""
     dev, (T, K), H = _device(z), pos.shape, z.shape[-1]
     code, wcode = _float_type(z), _real(weights)
@@ -696,7 +696,7 @@ def dense_moe_forward(layer: DenseLayer, x, bufs, y=None, aux: Optional[dict] = 
             return dense_moe_forward(layer, x, bufs, y, aux)
     ws = bufs["ws"]
     if y is None:
-        y = _new(x, x.shape, torch.int16, None)
+        y = torch.empty(x.shape, dtype=torch.int16, device=x.device)
     idx, gate = route(layer.desc, x, layer.w_router, ws)
     if aux is not None:
         aux["topk_idx"], aux["topk_gate"] = idx, gate

@@ -71,6 +71,17 @@ def test_dense_layer_matches_the_formula(shape, T):
     assert torch.equal(dpa.dense_moe_forward(layer, x, bufs), y)    # the same buffers again
 
 
+def test_dense_layer_as_the_first_call(monkeypatch):
+    # before any other call has looked up the element types
+    shape = W.TINY
+    layer = dpa.DenseLayer.from_host(dpa.make_desc(shape), *W.all_expert_weights(shape), W.router_weights(shape))
+    x = torch.from_numpy(W.tokens(shape, 3).view(np.int16)).cuda()
+    y = dpa.dense_moe_forward(layer, x, layer.buffers(3))
+    for name in ("_DTYPES", "_FLOATS", "_current_device", "_raw_stream", "_empty_like", "_empty_strided"):
+        monkeypatch.setattr(dpa, name, None)
+    assert torch.equal(dpa.dense_moe_forward(layer, x, layer.buffers(3)), y)
+
+
 def test_dense_layer_at_the_bitplane_layers_sizes():
     # Qwen3-shaped layer, batch 64: sampled tokens
     shape = W.QWEN3_B64
