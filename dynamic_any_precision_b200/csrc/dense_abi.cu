@@ -1,6 +1,7 @@
 // C ABI of the expert row sort and of the dense matrix products (include/dpa.h): validation and
 // launches.
 #include <atomic>
+#include <initializer_list>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -46,6 +47,27 @@ int sms_current() {
     return n;
 }
 
+// Bytes that a call reads or writes (none if the pointer is null).
+struct Span {
+    const void* at;
+    uint64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    if (!a.at || !b.at) return false;
+    const uint64_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x <= y ? y - x < a.bytes : x - y < b.bytes;
+}
+bool overlaps_any(const Span& out, std::initializer_list<Span> others) {
+    for (const Span& s : others)
+        if (overlap(out, s)) return true;
+    return false;
+}
+// `in` may be `out` itself, element for element, but lie across it in no other way
+bool lies_across(const Span& out, const Span& in) {
+    return overlap(out, in) && !(out.at == in.at && out.bytes == in.bytes);
+}
+uint64_t width(int dtype) { return dtype == DPA_DTYPE_FP64 ? 8 : dtype == DPA_DTYPE_FP32 ? 4 : 2; }
+
 dpa_status launched(cudaError_t e) { return e == cudaSuccess ? DPA_OK : DPA_ERR_CUDA; }
 
 dpa_status run_linear(const dpa_linear_desc* d, int groups, const void* x, const int32_t* offsets, const void* w,
@@ -62,6 +84,12 @@ dpa_status run_linear(const dpa_linear_desc* d, int groups, const void* x, const
     if (d->in_features % 8 || d->in_features > kMaxInputs) return DPA_ERR_UNSUPPORTED;   // rows of whole 16-byte pieces (tensor loads)
     if (d->rows > kMaxSide || d->out_features > kMaxSide) return DPA_ERR_UNSUPPORTED;
     if (ws_bytes < DPA_LINEAR_WORKSPACE_BYTES) return DPA_ERR_WORKSPACE;
+    const uint64_t M = d->rows, K = d->in_features, N = d->out_features, E = groups > 0 ? groups : 1;
+    const Span y{out, M * N * width(d->out_dtype)};
+    if (overlaps_any(y, {{x, M * K * 2}, {w, E * N * K * 2}, {w_mul, E * N * K * 2}, {bias, E * N * 2}, {bias_mul, E * N * 2},
+                         {offsets, (E + 1) * 4}, {ws, DPA_LINEAR_WORKSPACE_BYTES}}) ||
+        lies_across(y, {residual, M * N * width(d->residual_dtype)}))
+        return DPA_ERR_INVALID_ARG;
     dpa::LinearArgs a{};
     a.rows = d->rows;
     a.K = d->in_features;
@@ -97,7 +125,13 @@ dpa_status dpa_sort_pairs(const int32_t* idx, int n_pairs, int n_experts, int32_
     if (!given16(idx) || !given16(pos) || !given16(order) || !given16(offsets) || !given16(ws))
         return DPA_ERR_INVALID_ARG;
     if (n_pairs > kMaxPairs || n_experts > dpa::kSortMaxExperts) return DPA_ERR_UNSUPPORTED;
-    if (ws_bytes < dpa_sort_workspace_size(n_pairs, n_experts)) return DPA_ERR_WORKSPACE;
+    const size_t need = dpa_sort_workspace_size(n_pairs, n_experts);
+    if (ws_bytes < need) return DPA_ERR_WORKSPACE;
+    const uint64_t per = static_cast<uint64_t>(n_pairs) * 4;
+    const Span in{idx, per}, place{pos, per}, pair{order, per}, edge{offsets, (static_cast<uint64_t>(n_experts) + 1) * 4}, work{ws, need};
+    if (overlaps_any(place, {in, pair, edge, work}) || overlaps_any(pair, {in, edge, work}) || overlaps_any(edge, {in, work}) ||
+        overlap(in, work))
+        return DPA_ERR_INVALID_ARG;
     dpa::SortArgs a{};
     a.idx = idx;
     a.P = n_pairs;
@@ -114,6 +148,8 @@ dpa_status dpa_permute_rows(int dtype, const void* x, const int32_t* pos, int n_
     const dpa_status st = check_rows(n_tokens, top_k, hidden);
     if (st != DPA_OK) return st;
     if (!row_type(dtype) || !given16(x) || !given16(pos) || !given16(out)) return DPA_ERR_INVALID_ARG;
+    const uint64_t T = n_tokens, P = T * top_k, row = hidden * width(dtype);
+    if (overlaps_any({out, P * row}, {{x, T * row}, {pos, P * 4}})) return DPA_ERR_INVALID_ARG;
     return launched(dpa::launch_permute_pairs(dtype == DPA_DTYPE_FP32 ? 4 : 2, x, pos, n_tokens, top_k, hidden, out,
                                               static_cast<cudaStream_t>(stream), sms_current()));
 }
@@ -127,6 +163,11 @@ dpa_status dpa_unpermute_rows(int dtype, const void* z, const int32_t* pos, cons
     if (dtype != out_dtype && dtype != DPA_DTYPE_FP32 && out_dtype != DPA_DTYPE_FP32) return DPA_ERR_INVALID_ARG;
     if (residual && residual_dtype != out_dtype && residual_dtype != DPA_DTYPE_FP32) return DPA_ERR_INVALID_ARG;
     if (!given16(z) || !given16(pos) || !given16(y) || !opt16(residual) || !check_weights(weights, weight_dtype))
+        return DPA_ERR_INVALID_ARG;
+    const uint64_t T = n_tokens, P = T * top_k, H = hidden;
+    const Span out{y, T * H * width(out_dtype)};
+    if (overlaps_any(out, {{z, P * H * width(dtype)}, {pos, P * 4}, {weights, P * width(weight_dtype)}}) ||
+        lies_across(out, {residual, T * H * width(residual_dtype)}))
         return DPA_ERR_INVALID_ARG;
     dpa::UnpermuteArgs a{};
     a.z = z;
@@ -150,6 +191,12 @@ dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z,
     if (!row_type(dtype) || !given16(dy) || !given16(z) || !given16(pos) || !given16(dz) || !given16(dweights))
         return DPA_ERR_INVALID_ARG;
     if (!weights || !check_weights(weights, weight_dtype)) return DPA_ERR_INVALID_ARG;
+    const uint64_t T = n_tokens, P = T * top_k, row = hidden * width(dtype);
+    const Span rows{dz, P * row}, gates{dweights, P * 4};
+    const Span ins[] = {{dy, T * row}, {z, P * row}, {pos, P * 4}, {weights, P * width(weight_dtype)}};
+    if (overlap(rows, gates) || overlaps_any(rows, {ins[0], ins[2], ins[3]}) || lies_across(rows, ins[1]) ||
+        overlaps_any(gates, {ins[0], ins[1], ins[2], ins[3]}))
+        return DPA_ERR_INVALID_ARG;
     dpa::UnpermuteBwdArgs a{};
     a.dy = dy;
     a.z = z;

@@ -449,7 +449,8 @@ size_t dpa_sort_workspace_size(int n_pairs, int n_experts);
  *            expert in ascending order, unrouted pairs last;
  *   pos      int32 [n_pairs]: the place of each pair, -1 if it is not routed;
  *   offsets  int32 [n_experts + 1]: places before each expert; offsets[n_experts] = routed pairs.
- * Whole numbers, the same in every run. n_experts <= 1024, n_pairs <= 2^30. */
+ * Whole numbers, the same in every run. n_experts <= 1024, n_pairs <= 2^30. The outputs overlap
+ * neither idx nor one another. */
 dpa_status dpa_sort_pairs(const int32_t* idx, int n_pairs, int n_experts, int32_t* pos, int32_t* order,
                           int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
 
@@ -457,6 +458,7 @@ dpa_status dpa_sort_pairs(const int32_t* idx, int n_pairs, int n_experts, int32_
  * `dtype` (bf16, fp16, fp32); pos int32 [n_tokens][top_k] with distinct places, as dpa_sort_pairs
  * writes them. Places outside [0, n_tokens*top_k) are skipped; rows of out that no pair takes are
  * left as they were. Any hidden in 1 .. 2^24; top_k <= 32; n_tokens*top_k <= 2^30 (all row calls).
+ * Outputs overlap no input of their call, but where that is said (all row calls; refused).
  * Gradient: dpa_unpermute_rows without weights. */
 dpa_status dpa_permute_rows(int dtype, const void* x, const int32_t* pos, int n_tokens, int top_k, int hidden,
                             void* out, void* stream);
@@ -465,16 +467,17 @@ dpa_status dpa_permute_rows(int dtype, const void* x, const int32_t* pos, int n_
  * and rounded once. z [n_tokens*top_k][hidden] of `dtype`; weights [n_tokens][top_k] of
  * weight_dtype (fp32 or fp64; rounded to fp32) or NULL (all 1); residual [n_tokens][hidden] of
  * residual_dtype (out_dtype or fp32) or NULL, may be y itself; y [n_tokens][hidden] of out_dtype.
- * The types of z and y are equal, or one of them is fp32. Pairs with a place outside [0, n_tokens*top_k) add nothing (their row
- * of z is not read): a token without pairs gets its residual, or 0. */
+ * The types of z and y are equal, or one of them is fp32. Pairs with a place outside
+ * [0, n_tokens*top_k) add nothing (their row of z is not used): a token without pairs gets its
+ * residual, or 0. */
 dpa_status dpa_unpermute_rows(int dtype, const void* z, const int32_t* pos, const void* weights, int weight_dtype,
                               const void* residual, int residual_dtype, int out_dtype, int n_tokens, int top_k,
                               int hidden, void* y, void* stream);
 
 /* Gradients of dpa_unpermute_rows (device): dz[pos[t][k]] = weights[t][k] * dy[t] and
  * dweights[t][k] = <dy[t], z[pos[t][k]]> (fp32, 0 for pairs without a place). dy, z, dz of `dtype`;
- * pos with distinct places. Rows of dz that no pair takes are left as they were. The gradient of
- * the residual is dy. */
+ * pos with distinct places. dz may be z itself. Rows of dz that no pair takes are left as they were.
+ * The gradient of the residual is dy. */
 dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z, const int32_t* pos,
                                        const void* weights, int weight_dtype, int n_tokens, int top_k, int hidden,
                                        void* dz, float* dweights, void* stream);
@@ -484,10 +487,10 @@ dpa_status dpa_unpermute_rows_backward(int dtype, const void* dy, const void* z,
  * x [rows][in_features], w (and w_mul, U) [out_features][in_features], bias and bias_mul
  * [out_features], all of `dtype` (bf16 or fp16); out [rows][out_features] of out_dtype
  * (`dtype` or fp32); residual [rows][out_features] of residual_dtype (out_dtype or fp32), may be out
- * itself. bias, w_mul, bias_mul, residual may be
+ * itself in out's type. bias, w_mul, bias_mul, residual may be
  * NULL. Products are summed in fp32; out is rounded once. gelu is v*Phi(v), gelu_tanh its tanh
  * form. in_features must be a multiple of 8, at most 2^22; rows
- * and out_features in 1 .. 2^30. out overlaps no input but the residual.
+ * and out_features in 1 .. 2^30. out overlaps no input but the residual (refused).
  * ws: device, zero-filled once, at least DPA_LINEAR_WORKSPACE_BYTES (any workspace of this
  * library serves); it receives the device error flag only. */
 #define DPA_LINEAR_WORKSPACE_BYTES 256

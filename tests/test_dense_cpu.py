@@ -115,3 +115,45 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         dpa.linear(x, torch.zeros((8, 32), dtype=torch.bfloat16), ws)
     with pytest.raises(ValueError):
         dpa.grouped_linear(x, torch.zeros(3, dtype=torch.int32), torch.zeros((3, 8, 64), dtype=torch.bfloat16), ws)
+
+
+def test_overlapping_tensors_are_refused():
+    L = dpa.lib()
+
+    def at(kb):
+        return ctypes.c_void_p(1 << 30 | kb << 10)
+
+    far = [at(64 * i) for i in range(1, 10)]     # 64 KB apart; every tensor below is shorter
+    # sort: 1024 pairs (4 KB each), 8 experts
+    sort = [far[0], 1024, 8, far[1], far[2], far[3], far[4], 1 << 16, None]
+    for i, j in ((3, 0), (4, 0), (5, 0), (4, 3), (5, 3), (5, 4), (3, 6), (6, 0)):
+        for shift in (0, 16):
+            args = list(sort)
+            args[i] = ctypes.c_void_p(args[j].value + shift)
+            assert L.dpa_sort_pairs(*args) == 1, (i, j)
+    args = list(sort)
+    args[3] = ctypes.c_void_p(far[0].value + 4080)      # the last 16 bytes
+    assert L.dpa_sort_pairs(*args) == 1
+    # rows: 16 tokens of 4 slots, 64 elements of 2 bytes: 2 KB of tokens, 8 KB of rows
+    x, pos, out, w, r, dw = far[:6]
+
+    def by(p, n):
+        return ctypes.c_void_p(p.value + n)
+
+    for bad in (x, by(x, 2032), pos, by(x, -4096)):
+        assert L.dpa_permute_rows(0, x, pos, 16, 4, 64, bad, None) == 1
+    for bad in (x, by(x, 8176), pos, w, by(x, -2032), by(r, 16), by(r, -16)):
+        assert L.dpa_unpermute_rows(0, x, pos, w, 2, r, 0, 0, 16, 4, 64, bad, None) == 1
+    assert L.dpa_unpermute_rows(0, x, pos, w, 2, r, 2, 0, 16, 4, 64, r, None) == 1    # fp32 residual, 16-bit sums
+    dy, z = out, x
+    for dz, dg in ((dy, dw), (by(z, 16), dw), (by(z, -16), dw), (pos, dw), (w, dw), (r, by(r, 4096)), (r, z), (r, dy),
+                   (r, pos), (r, w)):
+        assert L.dpa_unpermute_rows_backward(0, dy, z, pos, w, 2, 16, 4, 64, dz, dg, None) == 1
+    # products: 16 rows, 64 inputs, 32 outputs, bf16 -> bf16 and fp32
+    for groups in (None, 4):
+        near = dict(x=far[0], w=far[1], b=far[2], u=far[3], c=far[4], r=far[5], ws=far[6], offsets=far[8])
+        for name in ("x", "w", "b", "u", "c", "ws") + (("offsets",) if groups else ()):
+            assert linear(desc=(16, 64, 32, 0, 0, 0, 0), groups=groups, out=near[name], **near) == 1, name
+        for shift in (16, -16):
+            assert linear(desc=(16, 64, 32, 0, 0, 0, 0), groups=groups, out=by(far[5], shift), **near) == 1
+        assert linear(desc=(16, 64, 32, 0, 0, 0, 2), groups=groups, out=far[5], **near) == 1

@@ -306,6 +306,17 @@ def test_row_gradients(T, K, E, H, drop, dtype):
         assert torch.equal(dw, dw2) and torch.equal(dz, dz2)
 
 
+@pytest.mark.parametrize("T,K,H", [(70, 8, 2048), (70, 3, 515), (300, 2, 66)])
+def test_row_gradients_in_place(T, K, H):
+    _, pos, _, live = sorted_rows(T, K, 16, 0.2, 8)
+    g = gen(11)
+    z, dy = normal(g, T * K, H, dtype=torch.bfloat16), normal(g, T, H, dtype=torch.bfloat16)
+    w = torch.rand((T, K), generator=g, device="cuda")
+    dz, dw = dpa.unpermute_rows_backward(dy, z, pos, w, dz=z.clone())
+    got, dw2 = dpa.unpermute_rows_backward(dy, z, pos, w, dz=z)
+    assert got is z and torch.equal(z, dz) and torch.equal(dw, dw2)
+
+
 def test_row_gradients_against_differences():
     # L = sum(c * y) is linear in z and in each weight: central differences in 64 bits of the
     # formula equal the gradient up to rounding
