@@ -81,7 +81,8 @@ dpa_status run_linear(const dpa_linear_desc* d, int groups, const void* x, const
     if (!given16(x) || !given16(w) || !given16(out) || !given16(ws)) return DPA_ERR_INVALID_ARG;
     if (!opt16(bias) || !opt16(w_mul) || !opt16(bias_mul) || !opt16(residual)) return DPA_ERR_INVALID_ARG;
     if (bias_mul && !w_mul) return DPA_ERR_INVALID_ARG;
-    if (d->in_features % 8 || d->in_features > kMaxInputs) return DPA_ERR_UNSUPPORTED;   // rows of whole 16-byte pieces (tensor loads)
+    // rows of whole 16-byte pieces (tensor loads)
+    if (d->in_features % 8 || d->in_features > kMaxInputs) return DPA_ERR_UNSUPPORTED;
     if (d->rows > kMaxSide || d->out_features > kMaxSide) return DPA_ERR_UNSUPPORTED;
     if (ws_bytes < DPA_LINEAR_WORKSPACE_BYTES) return DPA_ERR_WORKSPACE;
     const uint64_t M = d->rows, K = d->in_features, N = d->out_features, E = groups > 0 ? groups : 1;
@@ -128,9 +129,10 @@ dpa_status dpa_sort_pairs(const int32_t* idx, int n_pairs, int n_experts, int32_
     const size_t need = dpa_sort_workspace_size(n_pairs, n_experts);
     if (ws_bytes < need) return DPA_ERR_WORKSPACE;
     const uint64_t per = static_cast<uint64_t>(n_pairs) * 4;
-    const Span in{idx, per}, place{pos, per}, pair{order, per}, edge{offsets, (static_cast<uint64_t>(n_experts) + 1) * 4}, work{ws, need};
-    if (overlaps_any(place, {in, pair, edge, work}) || overlaps_any(pair, {in, edge, work}) || overlaps_any(edge, {in, work}) ||
-        overlap(in, work))
+    const Span in{idx, per}, place{pos, per}, pair{order, per}, work{ws, need};
+    const Span edge{offsets, (static_cast<uint64_t>(n_experts) + 1) * 4};
+    if (overlaps_any(place, {in, pair, edge, work}) || overlaps_any(pair, {in, edge, work}) ||
+        overlaps_any(edge, {in, work}) || overlap(in, work))
         return DPA_ERR_INVALID_ARG;
     dpa::SortArgs a{};
     a.idx = idx;

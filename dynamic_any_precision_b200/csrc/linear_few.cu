@@ -2,9 +2,10 @@
 // batch): bound by reading the weights once, and at these sizes (8 MB: 1.3 us of memory time) by
 // latency.
 //
-// A CTA computes 16 output features for all rows (grouped: for the rows of one non-empty group), its 4, 8 or 16 warps taking turns at blocks of 32 inputs.
-// Each lane reads 16-byte pieces of two weight rows straight into registers, all of a warp's loads
-// of a round in flight at once, with no shared memory, barrier or TMEM set-up in front of them. The
+// A CTA computes 16 output features for all rows (grouped: for the rows of one non-empty group), its
+// 4, 8 or 16 warps taking turns at blocks of 32 inputs. Each lane reads 16-byte pieces of two weight
+// rows straight into registers, all of a warp's loads of a round in flight at once, with no shared
+// memory, barrier or TMEM set-up in front of them. The
 // products go through m16n8k16 MMAs with the weight rows as M and the tokens as N; the tensor rate
 // does not matter here. The MMA's order of the 16 inputs is free as long as both operands use the
 // same one, so a lane's 16-byte piece (8 inputs) feeds two MMAs as it is. The warps' partial sums
@@ -69,8 +70,8 @@ __device__ __forceinline__ bool nonempty_group(const LinearArgs& a, int i, int l
 // NT tiles of 8 tokens at a time; MATS weight matrices (2: gated). Grid: feature blocks, groups (at
 // most as many as there are rows).
 template <bool F16, int MATS, int NT, bool GROUPED, int kWarps, bool PRECISE>
-__global__ void __launch_bounds__(kWarps * 32, kWarps == 16 ? 1 : (NT == 1 ? 3 : 2) * 8 / kWarps) few_rows_kernel(LinearArgs a, const uint16_t* x, const uint16_t* w,
-                                                               const uint16_t* u) {
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 16 ? 1 : (NT == 1 ? 3 : 2) * 8 / kWarps)
+few_rows_kernel(LinearArgs a, const uint16_t* x, const uint16_t* w, const uint16_t* u) {
     __shared__ float s_part[kWarps][MATS][8 * NT][kFeat + 1];
     constexpr int kRound = MATS * NT >= 4 ? 2 : 4;   // blocks whose loads are in flight together
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;

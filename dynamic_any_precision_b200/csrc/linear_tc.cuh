@@ -84,7 +84,9 @@ __host__ __device__ __forceinline__ int tile_rows(int n, int nt, int step) {
     const int each = nt == 1 ? n : (n - 1) / nt + 1;
     return (each + step - 1) / step * step;
 }
-__host__ __device__ __forceinline__ int balanced_rows(int n, int tn, int step) { return tile_rows(n, (n - 1) / tn + 1, step); }
+__host__ __device__ __forceinline__ int balanced_rows(int n, int tn, int step) {
+    return tile_rows(n, (n - 1) / tn + 1, step);
+}
 
 __device__ __forceinline__ int group_edge(const LinearArgs& a, int e) {
     return min(max(__ldg(a.offsets + e), 0), a.rows);   // an edge outside the rows reads as the nearest row

@@ -504,7 +504,8 @@ def sort_pairs(idx, n_experts: int, ws, pos=None, order=None, offsets=None, stre
         fp = offsets.data_ptr()
     else:
         fp = _arg(offsets, "offsets", (n_experts + 1,), "int32", dev)
-    _call(lib().dpa_sort_pairs, "dpa_sort_pairs", dev, stream, ip, P, n_experts, pp, op, fp, _workspace(ws, dev), ws.numel())
+    _call(lib().dpa_sort_pairs, "dpa_sort_pairs", dev, stream, ip, P, n_experts, pp, op, fp, _workspace(ws, dev),
+          ws.numel())
     return pos, order, offsets
 
 
@@ -623,8 +624,8 @@ def linear(x, w, ws, bias=None, act="none", w_mul=None, bias_mul=None, residual=
     """out = act(x w^T + bias) [* (x w_mul^T + bias_mul)] [+ residual]. x: [M][K] bf16 (or int16
     bits) or fp16, K a multiple of 8; w, w_mul: [N][K]; bias, bias_mul: [N], all of x's type; out:
     [M][N] in x's type or fp32 (out_dtype; default: residual's, else x's); residual: [M][N] of
-    out's type or fp32, may be `out`. act: "none", "relu", "gelu", "gelu_tanh" or "silu". ws: new_linear_workspace or any
-    other workspace; it receives the device error flag."""
+    out's type or fp32, may be `out`. act: "none", "relu", "gelu", "gelu_tanh" or "silu". ws:
+    new_linear_workspace or any other workspace; it receives the device error flag."""
     return _product(lib().dpa_linear, "dpa_linear", x, w, (), (), ws, bias, act, w_mul, bias_mul, residual, out,
                     out_dtype, stream)
 
