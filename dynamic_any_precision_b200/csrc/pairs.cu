@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
     int32_t* s_warp = smem;               // [nw][E1] counts, later the first place
     int32_t* s_tot = smem + nw * E1;      // [E1] pairs of the key in all chunks, later the key's start
     int32_t* s_pre = s_tot + E1;          // [E1] pairs of the key in earlier chunks
-    __shared__ int32_t s_sum[32];
+    int32_t* s_sum = s_pre + E1;          // [32] totals of each warp's keys
     for (int i = threadIdx.x; i < (nw + 2) * E1; i += blockDim.x) smem[i] = 0;
     const bool alone = gridDim.x == 1;
     if (alone) pdl_wait();
@@ -200,7 +200,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
     }
 }
 
-size_t sort_smem_bytes(int warps, int E) { return static_cast<size_t>(warps + 2) * (E + 1) * 4; }
+// All of sort_place_kernel's shared memory is dynamic, so that this size alone decides whether it
+// passes the 48 KB that a launch may ask for without a raised limit.
+size_t sort_smem_bytes(int warps, int E) { return static_cast<size_t>(warps + 2) * (E + 1) * 4 + 32 * 4; }
 
 // ---------------------------------------------------------------- rows
 
@@ -862,13 +864,8 @@ cudaError_t launch_sort_pairs(const SortArgs& a, cudaStream_t stream) {
     SortArgs b = a;
     b.chunk = sort_chunk_pairs(a.P);
     const int nb = (a.P - 1) / b.chunk + 1;
-    void* args[] = {&b};
     int threads = kSortThreads;
-    if (nb > 1) {
-        const cudaError_t err = launch_pdl_raw(reinterpret_cast<const void*>(sort_count_kernel), dim3(nb),
-                                               dim3(kSortThreads), static_cast<size_t>(a.E + 1) * 4, stream, args);
-        if (err != cudaSuccess) return err;
-    } else {
+    if (nb == 1) {
         // a warp per 32 pairs, and at least four for the scan over the experts
         threads = ((a.P + 31) / 32) * 32;
         threads = threads < 128 ? 128 : threads > kSortThreads ? kSortThreads : threads;
@@ -879,10 +876,16 @@ cudaError_t launch_sort_pairs(const SortArgs& a, cudaStream_t stream) {
                      : rounds <= 8 ? reinterpret_cast<const void*>(sort_place_kernel<8>)
                                    : reinterpret_cast<const void*>(sort_place_kernel<0>);
     const size_t smem = sort_smem_bytes(threads / 32, a.E);
-    if (smem > 48 * 1024) {
+    if (smem > 48 * 1024) {   // before the first launch: an error leaves nothing launched
         const cudaError_t err =
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(sort_smem_bytes(kSortThreads / 32, kSortMaxExperts)));
+        if (err != cudaSuccess) return err;
+    }
+    void* args[] = {&b};
+    if (nb > 1) {
+        const cudaError_t err = launch_pdl_raw(reinterpret_cast<const void*>(sort_count_kernel), dim3(nb),
+                                               dim3(kSortThreads), static_cast<size_t>(a.E + 1) * 4, stream, args);
         if (err != cudaSuccess) return err;
     }
     return launch_pdl_raw(fn, dim3(nb), dim3(threads), smem, stream, args);
