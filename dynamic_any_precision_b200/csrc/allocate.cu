@@ -1147,8 +1147,7 @@ cudaError_t launch_allocate(const AllocArgs& a, cudaStream_t stream, CoopSync* c
         cudaError_t err = cudaMemsetAsync(coop, 0, sizeof(CoopSync), stream);
         if (err != cudaSuccess) return err;
         if (smem > 48 * 1024) {
-            err = cudaFuncSetAttribute(allocate_coop_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+            err = allow_dynamic_smem(reinterpret_cast<const void*>(allocate_coop_kernel), smem);
             if (err != cudaSuccess) return err;
         }
         cudaLaunchConfig_t cfg = {};
@@ -1172,8 +1171,7 @@ cudaError_t launch_allocate(const AllocArgs& a, cudaStream_t stream, CoopSync* c
         // the grouping's layout, then every pair's costs, the pair list and the final counts
         const size_t smem = allocate_smem_bytes(P, a.E, nk, a.vrec != nullptr) + static_cast<size_t>(P) * nk * 8 +
                             static_cast<size_t>(P) * 5;
-        cudaError_t err = cudaFuncSetAttribute(allocate_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+        cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void*>(allocate_cluster_kernel), smem);
         if (err != cudaSuccess) return err;
         if (kClCtas > 8) {
             err = cudaFuncSetAttribute(allocate_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1198,8 +1196,7 @@ cudaError_t launch_allocate(const AllocArgs& a, cudaStream_t stream, CoopSync* c
     }
     const size_t smem = allocate_smem_bytes(P, a.E, nk, a.vrec != nullptr);
     if (smem > 48 * 1024) {
-        cudaError_t err = cudaFuncSetAttribute(allocate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+        cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void*>(allocate_kernel), smem);
         if (err != cudaSuccess) return err;
     }
     void* args[] = {&b};

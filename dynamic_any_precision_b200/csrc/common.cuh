@@ -2,6 +2,8 @@
 // mbarrier waits, bulk global->shared copies, MMA wrappers.
 #pragma once
 #include <cstdint>
+#include <mutex>
+
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -237,6 +239,27 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
 // CTAs take SM slots from a wide predecessor.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Lets launches of `fn` take `bytes` of dynamic shared memory on the current device. The limit belongs to
+// the function, so it never goes down: host threads launch the same kernel with different sizes, and one
+// must not lower it between another's call of this and its launch.
+inline cudaError_t allow_dynamic_smem(const void* fn, size_t bytes) {
+    struct Limit {
+        const void* fn;
+        size_t bytes;
+    };
+    constexpr int kMost = 256;   // kernels of this library that call this: fewer than half as many
+    static std::mutex mu;
+    static Limit known[kMost];
+    std::lock_guard<std::mutex> lock(mu);
+    int i = 0;
+    while (i < kMost && known[i].fn && known[i].fn != fn) ++i;
+    if (i == kMost) return cudaErrorUnknown;
+    const size_t limit = known[i].bytes > bytes ? known[i].bytes : bytes;
+    const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(limit));
+    if (err == cudaSuccess) known[i] = {fn, limit};
+    return err;
+}
 
 // Launch with programmatic stream serialisation (see above).
 inline cudaError_t launch_pdl_raw(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,

@@ -765,7 +765,7 @@ template <int FMT, int NRT, int NTILE, int NMAT>
 cudaError_t launch_variant(const VpArgs& a, cudaStream_t stream, int sms) {
     const VLayout L = vlayout<NRT, NTILE, NMAT>(a.K, a.G, FMT, a.B);
     const void* fn = reinterpret_cast<const void*>(vp_gemv_kernel<FMT, NRT, NTILE, NMAT>);
-    cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L.total));
+    cudaError_t err = allow_dynamic_smem(fn, L.total);
     if (err != cudaSuccess) return err;
     const int items = a.max_groups * (a.R / (16 * NRT));
     const int grid = items < sms ? (items > 0 ? items : 1) : sms;

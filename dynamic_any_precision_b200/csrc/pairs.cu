@@ -804,7 +804,7 @@ cudaError_t unpermute_types(const UnpermuteArgs& a, cudaStream_t stream, int sms
         const int ctas = fed < per_sm * sms ? static_cast<int>(fed) : per_sm * sms;
         const void* fn = whole ? reinterpret_cast<const void*>(unpermute_stream_kernel<ZT, YT, RT>)
                                : reinterpret_cast<const void*>(unpermute_shift_kernel<ZT, YT, RT>);
-        const cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t err = allow_dynamic_smem(fn, static_cast<size_t>(smem));   // with or without a residual
         if (err != cudaSuccess) return err;
         int r = runs;
         void* sargs[] = {&b, &r, &stage_bytes};

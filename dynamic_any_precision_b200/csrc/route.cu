@@ -1034,8 +1034,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int sms) {
         if (err != cudaSuccess) return err;
         size_t ssm = (static_cast<size_t>(a.E) * 24 + 15) & ~static_cast<size_t>(15);
         if (ssm > 48 * 1024) {
-            err = cudaFuncSetAttribute(route_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(ssm));
+            err = allow_dynamic_smem(reinterpret_cast<const void*>(route_select_kernel), ssm);
             if (err != cudaSuccess) return err;
         }
         void* args[] = {&b};
@@ -1056,7 +1055,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int sms) {
                              : (nq <= 4 ? reinterpret_cast<const void*>(route_kernel<4>)
                                         : reinterpret_cast<const void*>(route_kernel<8>));
     if (smem > 48 * 1024) {
-        cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaError_t err = allow_dynamic_smem(fn, smem);
         if (err != cudaSuccess) return err;
     }
     dim3 grid(chunks, a.T);

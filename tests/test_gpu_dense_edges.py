@@ -3,10 +3,14 @@ pass by."""
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 
 torch = pytest.importorskip("torch")
+
+from dynamic_any_precision_b200 import dpa  # noqa: E402
+from test_gpu_dense import gen, normal  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +41,35 @@ def test_sorts_that_take_48_kb():
     # in a process of its own: a larger sort before them would have raised the kernels' limit
     got = subprocess.run([sys.executable, "-c", SORTS], capture_output=True, text=True, timeout=300)
     assert got.returncode == 0 and "sorted" in got.stdout, got.stdout + got.stderr
+
+
+# ------------------------------------------------------------------------------ host threads
+
+def test_two_host_threads_launch_the_same_kernel_with_different_sizes():
+    # the row sums' ring is larger with a residual; neither thread may lower the kernel's limit under
+    # the other (rows of whole 16-byte pieces and others: two kernels)
+    call = dpa.lib().dpa_unpermute_rows     # without the binding's work between two calls
+    for T, K, H in ((1300, 2, 2047), (1300, 2, 2048)):
+        g = gen(H)
+        z, res = normal(g, T * K, H, dtype=torch.bfloat16), normal(g, T, H)
+        pos = torch.randperm(T * K, generator=g, device="cuda").int().view(T, K)
+        want = [dpa.unpermute_rows(z, pos, residual=r, out_dtype=torch.float32) for r in (res, None)]
+        got = [torch.empty((T, H), device="cuda") for _ in want]
+        torch.cuda.synchronize()
+        codes = [set(), set()]
+
+        def run(i, residual):
+            stream = torch.cuda.Stream()
+            args = (dpa.DTYPE_BF16, z.data_ptr(), pos.data_ptr(), None, -1, residual, dpa.DTYPE_FP32, dpa.DTYPE_FP32, T, K,
+                    H, got[i].data_ptr(), stream.cuda_stream)
+            for n in range(200):
+                codes[i].update([call(*args) for _ in range(100)])
+                stream.synchronize()
+
+        threads = [threading.Thread(target=run, args=a) for a in ((0, res.data_ptr()), (1, None))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert codes == [{0}, {0}]
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
