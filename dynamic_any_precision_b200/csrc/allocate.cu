@@ -1146,7 +1146,7 @@ cudaError_t launch_allocate(const AllocArgs& a, cudaStream_t stream, CoopSync* c
         const size_t smem = static_cast<size_t>(per_block) * 32;
         cudaError_t err = cudaMemsetAsync(coop, 0, sizeof(CoopSync), stream);
         if (err != cudaSuccess) return err;
-        if (smem > 48 * 1024) {
+        if (smem > kDefaultDynamicSmem) {
             err = allow_dynamic_smem(reinterpret_cast<const void*>(allocate_coop_kernel), smem);
             if (err != cudaSuccess) return err;
         }
@@ -1195,7 +1195,7 @@ cudaError_t launch_allocate(const AllocArgs& a, cudaStream_t stream, CoopSync* c
         return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(allocate_cluster_kernel), cargs);
     }
     const size_t smem = allocate_smem_bytes(P, a.E, nk, a.vrec != nullptr);
-    if (smem > 48 * 1024) {
+    if (smem > kDefaultDynamicSmem) {
         cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void*>(allocate_kernel), smem);
         if (err != cudaSuccess) return err;
     }

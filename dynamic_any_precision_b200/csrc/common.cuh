@@ -261,6 +261,10 @@ inline cudaError_t allow_dynamic_smem(const void* fn, size_t bytes) {
     return err;
 }
 
+// Dynamic bytes that a kernel may take without allow_dynamic_smem: 48 KB less its static shared memory,
+// which counts against the same default (at most 8 KB in the kernels that take both).
+constexpr size_t kDefaultDynamicSmem = 40 * 1024;
+
 // Launch with programmatic stream serialisation (see above).
 inline cudaError_t launch_pdl_raw(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                                   void** args) {

@@ -200,8 +200,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
     }
 }
 
-// All of sort_place_kernel's shared memory is dynamic, so that this size alone decides whether it
-// passes the 48 KB that a launch may ask for without a raised limit.
+// All of sort_place_kernel's shared memory (none is static).
 size_t sort_smem_bytes(int warps, int E) { return static_cast<size_t>(warps + 2) * (E + 1) * 4 + 32 * 4; }
 
 // ---------------------------------------------------------------- rows
@@ -876,7 +875,7 @@ cudaError_t launch_sort_pairs(const SortArgs& a, cudaStream_t stream) {
                      : rounds <= 8 ? reinterpret_cast<const void*>(sort_place_kernel<8>)
                                    : reinterpret_cast<const void*>(sort_place_kernel<0>);
     const size_t smem = sort_smem_bytes(threads / 32, a.E);
-    if (smem > 48 * 1024) {   // before the first launch: an error leaves nothing launched
+    if (smem > kDefaultDynamicSmem) {   // before the first launch: an error leaves nothing launched
         const cudaError_t err =
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(sort_smem_bytes(kSortThreads / 32, kSortMaxExperts)));

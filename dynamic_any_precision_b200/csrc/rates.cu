@@ -130,7 +130,7 @@ size_t rates_smem_bytes(int E, int nk) { return static_cast<size_t>(E) * nk * 8;
 
 cudaError_t launch_solve_rates(const RatesArgs& a, cudaStream_t stream) {
     const size_t smem = rates_smem_bytes(a.E, a.kmax - a.kmin + 1);
-    if (smem > 48 * 1024) {
+    if (smem > kDefaultDynamicSmem) {
         cudaError_t err = allow_dynamic_smem(reinterpret_cast<const void*>(solve_rates_kernel), smem);
         if (err != cudaSuccess) return err;
     }

@@ -1033,7 +1033,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int sms) {
         else err = launch_route_prep<64, 128>(b, r, stream);
         if (err != cudaSuccess) return err;
         size_t ssm = (static_cast<size_t>(a.E) * 24 + 15) & ~static_cast<size_t>(15);
-        if (ssm > 48 * 1024) {
+        if (ssm > kDefaultDynamicSmem) {
             err = allow_dynamic_smem(reinterpret_cast<const void*>(route_select_kernel), ssm);
             if (err != cudaSuccess) return err;
         }
@@ -1054,7 +1054,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream, int sms) {
     const void* fn = nq <= 2 ? reinterpret_cast<const void*>(route_kernel<2>)
                              : (nq <= 4 ? reinterpret_cast<const void*>(route_kernel<4>)
                                         : reinterpret_cast<const void*>(route_kernel<8>));
-    if (smem > 48 * 1024) {
+    if (smem > kDefaultDynamicSmem) {
         cudaError_t err = allow_dynamic_smem(fn, smem);
         if (err != cudaSuccess) return err;
     }

@@ -37,10 +37,50 @@ print("sorted")
 """
 
 
+def in_a_process_of_its_own(code, says):
+    # a larger call before it would have raised the kernels' limits
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and says in got.stdout, got.stdout + got.stderr
+
+
 def test_sorts_that_take_48_kb():
-    # in a process of its own: a larger sort before them would have raised the kernels' limit
-    got = subprocess.run([sys.executable, "-c", SORTS], capture_output=True, text=True, timeout=300)
-    assert got.returncode == 0 and "sorted" in got.stdout, got.stdout + got.stderr
+    in_a_process_of_its_own(SORTS, "sorted")
+
+
+# The other kernels whose shared memory may lie just below 48 KB: the router of one token (12 bytes per
+# input and 1376 static) and the allocation of one CTA (uniform control; 7808 static).
+DECISIONS = f"""
+import sys
+sys.path[:0] = [{ROOT!r}]
+import numpy as np, torch
+from dynamic_any_precision_b200 import dpa, workloads as W
+from oracle import dpa_oracle as O
+for H in (4032, 4096):
+    shape = W.with_sizes(W.TINY, hidden=H, name="one_token")
+    x, wr = W.tokens(shape, 1), W.router_weights(shape)
+    desc = dpa.make_desc(shape)
+    idx, gate = dpa.route(desc, torch.from_numpy(x.view(np.int16)).cuda(), torch.from_numpy(wr.view(np.int16)).cuda(),
+                          dpa.new_workspace(desc, 1))
+    want = O.route(x, wr, shape.top_k, shape.norm_topk)
+    assert np.array_equal(idx.cpu().numpy(), want[0]) and np.array_equal(gate.cpu().numpy(), want[1]), H
+shape = W.with_sizes(W.TINY, n_experts=128, top_k=8, name="pairs")
+desc = dpa.make_desc(shape)
+rng = np.random.default_rng(5)
+rtable = np.sort(rng.random((128, 4)), 1)[:, ::-1].copy()
+for T in (165, 180, 198):
+    idx = rng.integers(0, 128, (T, 8)).astype(np.int32)
+    gate = rng.random((T, 8))
+    k, _ = dpa.allocate(desc, *(torch.from_numpy(a).cuda() for a in (rtable, idx, gate)),
+                        torch.tensor([2.625], dtype=torch.float64, device="cuda"), dpa.new_workspace(desc, T),
+                        policy=dpa.ALLOC_UNIFORM)
+    want = O.allocate_uniform(T * 8, shape.kmin, shape.kmax, 2.625)
+    assert np.array_equal(k.cpu().numpy().reshape(-1), want), T
+print("decided")
+"""
+
+
+def test_routing_and_allocation_that_take_48_kb():
+    in_a_process_of_its_own(DECISIONS, "decided")
 
 
 # ------------------------------------------------------------------------------ host threads
