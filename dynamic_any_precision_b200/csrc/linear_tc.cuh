@@ -528,6 +528,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
                     }
                 }
             }
+            // The last arrival on every stage's barrier lands before this CTA may end (the MMA warp of the
+            // pair's first CTA sends them to both CTAs' shared memory).
+            for (int i = 0; i < stages && ok; ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait_abortable(&empty[s], ph, s_abort, a.hdr, 0x711));
+                if (++s == stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
             if (*s_abort) {   // copies already issued land well within this time
                 const uint64_t t0 = globaltimer();
                 while (globaltimer() - t0 < 2000000ull) __nanosleep(10000);
@@ -789,7 +798,13 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();   // both CTAs are done with the pair's barriers and TMEM
+    if constexpr (CG == 2) {
+        // the first CTA's last commit arrives here too (not waited for earlier: the time limit of a wait is
+        // meant for a tile, not for all of them)
+        if (warp == kMmaWarp && rank == 1) mbar_wait_bounded(done, 0, a.hdr, 0x723);
+        __syncwarp();
+        cluster_sync();   // both CTAs are done with the pair's barriers and TMEM
+    }
     if (warp == kMmaWarp) {
         tc_fence_after();
         if constexpr (CG == 1)

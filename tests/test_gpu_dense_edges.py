@@ -113,3 +113,33 @@ def test_two_host_threads_launch_the_same_kernel_with_different_sizes():
             t.join()
         assert codes == [{0}, {0}]
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# --------------------------------------------------------------------------------- products
+
+def test_pairs_of_blocks_back_to_back():
+    # products by CTA pairs one right after another and on two streams at once, so that a pair's shared
+    # memory is taken over as soon as both of its CTAs have ended
+    g = gen(4)
+    shapes = [(700, 264, 4100), (257, 64, 9473), (2000, 1024, 2500), (600, 520, 2504)]
+    inputs = [(normal(g, r, k, dtype=torch.bfloat16), normal(g, n, k, dtype=torch.bfloat16, scale=k ** -0.5))
+              for r, k, n in shapes]
+    spaces = [dpa.new_linear_workspace() for _ in range(3)]
+    want = [dpa.linear(x, w, spaces[2], act="silu", w_mul=w) for x, w in inputs]
+    for (x, w), y in zip(inputs, want):
+        v = x.double() @ w.double().T
+        ref = v * v * torch.sigmoid(v)
+        assert float((y.double() - ref).norm() / ref.norm()) < 2.0 ** -8    # one rounding to bf16
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for s, ws, out in zip(streams, spaces, got):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(30):
+                out.append([dpa.linear(x, w, ws, act="silu", w_mul=w) for x, w in inputs])
+    torch.cuda.synchronize()
+    assert all(dpa.device_status(ws) == 0 for ws in spaces)
+    for out in got:
+        for ys in out:
+            for y, ref in zip(ys, want):
+                assert torch.equal(y, ref)
