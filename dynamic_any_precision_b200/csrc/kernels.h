@@ -282,6 +282,12 @@ struct LinearArgs {
     // feature tiles)
     int ksteps, FT, TN, splits, stages, xbox, ntiles, out_bytes, out_wide, step_t, step_f;
 };
+// Sums so long that 16-bit outputs, too, would see what the tensor cores drop when they add without
+// rounding (7e-10 of the sum per input, with a gate twice that: at this border a tenth of fp16's half unit
+// 2^-11, at 2^20 inputs 1.5 of it, and 3 with a gate). They are added in blocks, as those of fp32 outputs.
+inline bool long_sums(const LinearArgs& a, bool gated) {
+    return a.K > (gated || a.act != DPA_ACT_NONE ? 1 << 15 : 1 << 16);
+}
 cudaError_t launch_linear(const LinearArgs& a, bool f16, const void* x, const void* w, const void* w_mul,
                           cudaStream_t stream, int sms);
 // The products of few rows (linear_few.cu): at most 32 plain ones, or 64 that lie in few per group.

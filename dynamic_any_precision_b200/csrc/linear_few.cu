@@ -126,7 +126,7 @@ few_rows_kernel(LinearArgs a, const uint16_t* x, const uint16_t* w, const uint16
                         }
             };
             if constexpr (PRECISE) {
-                // fp32 outputs: a round's products are summed by themselves and added with rounding;
+                // fp32 outputs, very long sums: a round's products are summed by themselves and added with rounding;
                 // the MMA drops the bits below its accumulator's last place at every step, which
                 // would grow with K
                 float part[MATS][NT][4] = {};
@@ -206,7 +206,7 @@ cudaError_t launch_linear_few(const LinearArgs& a, bool f16, const void* x, cons
     const int64_t ctas = static_cast<int64_t>(blocks) * groups;
     int warps = ctas <= 3 * sms && a.K > 512 ? 8 : 4;
     if (!grouped && ctas <= sms && a.K > 1024 && a.rows <= 16) warps = 16;
-    const bool precise = a.out32;
+    const bool precise = a.out32 || long_sums(a, w_mul != nullptr);
     const void* fn = w_mul ? (f16 ? pick<true, 2>(grouped, a.rows, warps, precise) : pick<false, 2>(grouped, a.rows, warps, precise))
                            : (f16 ? pick<true, 1>(grouped, a.rows, warps, precise) : pick<false, 1>(grouped, a.rows, warps, precise));
     LinearArgs b = a;

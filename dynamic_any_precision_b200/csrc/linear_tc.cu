@@ -119,11 +119,12 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
     int64_t clusters;
     // K blocks: the tensor cores drop the bits below the accumulator's last place at every step of 16
     // inputs, which takes about 1e-9 of the sum per input away (K = 8192: 9e-6; with a gate twice
-    // that). 16-bit outputs do not see it. For fp32 outputs of more than 768 inputs (512 with an
+    // that). 16-bit outputs see it in very long sums only (long_sums). For fp32 outputs of more than 768 inputs (512 with an
     // activation, 256 with a gate, which widen the error) blocks of 256 are added in fp32 with
     // rounding: 3e-7 whatever K. The running sums take a third of tensor memory, so a tile has at most
     // 160 tokens then.
-    const bool blocks = a.out32 && a.ksteps > (gated ? 4 : a.act != DPA_ACT_NONE ? 8 : 12);
+    const bool blocks =
+        a.out32 ? a.ksteps > (gated ? 4 : a.act != DPA_ACT_NONE ? 8 : 12) : long_sums(a, gated);
     if (a.E > 0) {
         a.TN = pair && !blocks ? 256 : 128;
         a.xbox = 16;

@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from dynamic_any_precision_b200 import dpa  # noqa: E402
-from test_gpu_dense import gen, normal  # noqa: E402
+from test_gpu_dense import DT, close, gen, normal  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,30 @@ def test_pairs_of_blocks_back_to_back():
         for ys in out:
             for y, ref in zip(ys, want):
                 assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("rows,N,dtype", [(16, 400, "fp16"), (40, 40, "fp16"), (300, 200, "fp16"), (300, 200, "bf16"),
+                                          (2560, 1024, "fp16")])
+@pytest.mark.parametrize("gated", [False, True])
+def test_16_bit_outputs_of_very_long_sums(rows, N, dtype, gated):
+    # Positive terms, so that the sum is its own magnitude. Blocks of 256 inputs (17 steps of two roundings
+    # or truncations, 2^-23 of the block each) are added with rounding, 2^-24 of the sum each (few rows:
+    # blocks of 64 inputs or more per warp, 16 warps at most); the output is rounded once.
+    K, dt = 1 << 18, DT[dtype]
+    g = gen(rows + N)
+    x = ((torch.rand((rows, K), generator=g, device="cuda") + 0.5) * 2.0 ** -9).to(dt)
+    w = ((torch.rand((N, K), generator=g, device="cuda") + 0.5) * 2.0 ** -8).to(dt)
+    ws = dpa.new_linear_workspace()
+    y = dpa.linear(x, w, ws, w_mul=w if gated else None)
+    pick = slice(None) if rows <= 300 else slice(0, None, 40)
+    ref = x[pick].double() @ w.double().T
+    part = 34 * 2.0 ** -23 + (K / 256 + 16) * 2.0 ** -24
+    if gated:
+        ref, part = ref * ref, 2 * part + part * part
+    close(y[pick], ref, (part + torch.finfo(dt).eps / 2 * (1 + part)) * ref)
+    if rows <= 40:
+        off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device="cuda")
+        w2 = torch.stack((w, w))
+        got = dpa.grouped_linear(x, off, w2, ws, w_mul=w2 if gated else None)
+        close(got, ref, (part + torch.finfo(dt).eps / 2 * (1 + part)) * ref)
+    assert dpa.device_status(ws) == 0
