@@ -249,7 +249,8 @@ __device__ __forceinline__ Slots load_slots(const int32_t* pos, const void* weig
 
 // A pack if `on`, else zeros. Written as predicated loads so that the loads of several rows stay
 // together in front of the arithmetic (as branches they were moved to their uses, one at a time:
-// 136 against 41 us for 4096 tokens of 8 rows of 2048 bf16).
+// 136 against 41 us for 4096 tokens of 8 rows of 2048 bf16). Outputs may lie on inputs (a residual, the
+// rows' gradient): the compiler must not move a store in front of them, hence "memory".
 template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_if(const T* p, bool on) {
     constexpr int kBytes = sizeof(T) * VEC;
@@ -264,7 +265,8 @@ __device__ __forceinline__ Pack<T, VEC> load_if(const T* p, bool on) {
                 "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
                 "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
                 : "=&r"(r[i].x), "=&r"(r[i].y), "=&r"(r[i].z), "=&r"(r[i].w)
-                : "l"(reinterpret_cast<const char*>(p) + 16 * i), "r"(static_cast<uint32_t>(on)));
+                : "l"(reinterpret_cast<const char*>(p) + 16 * i), "r"(static_cast<uint32_t>(on))
+                : "memory");
         memcpy(&out, r, kBytes);
     } else if constexpr (kBytes == 8) {
         uint2 r;
@@ -274,7 +276,8 @@ __device__ __forceinline__ Pack<T, VEC> load_if(const T* p, bool on) {
             "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
             "@p ld.global.v2.b32 {%0, %1}, [%2];\n\t}"
             : "=&r"(r.x), "=&r"(r.y)
-            : "l"(p), "r"(static_cast<uint32_t>(on)));
+            : "l"(p), "r"(static_cast<uint32_t>(on))
+            : "memory");
         memcpy(&out, &r, kBytes);
     } else if constexpr (kBytes == 4) {
         uint32_t r;
@@ -284,7 +287,8 @@ __device__ __forceinline__ Pack<T, VEC> load_if(const T* p, bool on) {
             "mov.b32 %0, 0;\n\t"
             "@p ld.global.b32 %0, [%1];\n\t}"
             : "=&r"(r)
-            : "l"(p), "r"(static_cast<uint32_t>(on)));
+            : "l"(p), "r"(static_cast<uint32_t>(on))
+            : "memory");
         memcpy(&out, &r, kBytes);
     } else {
         uint16_t r;
@@ -294,7 +298,8 @@ __device__ __forceinline__ Pack<T, VEC> load_if(const T* p, bool on) {
             "mov.b16 %0, 0;\n\t"
             "@p ld.global.b16 %0, [%1];\n\t}"
             : "=&h"(r)
-            : "l"(p), "r"(static_cast<uint32_t>(on)));
+            : "l"(p), "r"(static_cast<uint32_t>(on))
+            : "memory");
         memcpy(&out, &r, kBytes);
     }
     return out;

@@ -10,7 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from dynamic_any_precision_b200 import dpa  # noqa: E402
-from test_gpu_dense import DT, close, gen, normal  # noqa: E402
+from test_gpu_dense import DT, close, gen, normal, sorted_rows  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -113,6 +113,27 @@ def test_two_host_threads_launch_the_same_kernel_with_different_sizes():
             t.join()
         assert codes == [{0}, {0}]
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------------------------- rows
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,K,H", [(9000, 2, 72), (40, 17, 515), (1500, 8, 2047), (33, 4, 4096), (5000, 1, 130)])
+def test_row_gradients_over_their_own_rows(T, K, H, dtype):
+    # every kernel form (slots at a time, elements per load, warps per token) with dz = z
+    _, pos, _, _ = sorted_rows(T, K, 16, 0.2, T + K)
+    g = gen(T + H)
+    z, dy = normal(g, T * K, H, dtype=DT[dtype]), normal(g, T, H, dtype=DT[dtype])
+    w = torch.rand((T, K), generator=g, device="cuda")
+    dz, dw = dpa.unpermute_rows_backward(dy, z, pos, w, dz=z.clone())
+    keep = z.clone()
+    assert torch.equal(dpa.unpermute_rows_backward(dy, z, pos, w, dz=torch.empty_like(z))[1], dw)
+    assert torch.equal(z, keep)
+    got, dw2 = dpa.unpermute_rows_backward(dy, z, pos, w, dz=z)
+    assert got is z and torch.equal(z, dz) and torch.equal(dw, dw2)
+    on = pos >= 0
+    prod = torch.where(on[:, :, None], keep[pos.clamp_min(0).long()].double() * dy.double()[:, None, :], 0.0)
+    close(dw, prod.sum(2), (H + 1) * 2.0 ** -24 * prod.abs().sum(2))
 
 
 # --------------------------------------------------------------------------------- products
