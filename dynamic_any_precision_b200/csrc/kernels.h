@@ -277,9 +277,9 @@ struct LinearArgs {
     int act, out32, res32;    // DPA_ACT_*; 1: fp32 output, fp32 residual
     WsHeader* hdr;
     // set by the launcher: K steps, feature tiles, most tokens per tile, CTAs sharing K, pipeline
-    // stages, rows of the smallest token load, tiles (plain), bytes of the epilogue's shared memory,
-    // whether out is 32-byte aligned, and how far a cluster's next tile lies (token tiles, then
-    // feature tiles)
+    // stages, rows of the smallest token load, tiles (grouped: the most there can be), bytes of the
+    // epilogue's shared memory, whether out is 32-byte aligned, and how far a cluster's next tile lies
+    // (token tiles, then feature tiles)
     int ksteps, FT, TN, splits, stages, xbox, ntiles, out_bytes, out_wide, step_t, step_f;
 };
 // Sums so long that 16-bit outputs, too, would see what the tensor cores drop when they add without

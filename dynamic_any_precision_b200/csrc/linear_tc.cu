@@ -132,6 +132,7 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
         const int64_t tiles =
             (static_cast<int64_t>(a.rows) / a.TN + (a.rows < a.E ? a.rows : a.E)) * a.FT;
         if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+        a.ntiles = static_cast<int>(tiles);
         if (!pair) a.splits = split_k(tiles, a.ksteps);
         clusters = a.splits > 1 ? tiles : (sms / CG < tiles ? sms / CG : tiles);
     } else {

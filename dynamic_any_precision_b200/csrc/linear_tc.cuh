@@ -25,6 +25,7 @@
 // addition to the running sums) overlaps the next one's MMAs. Every wait is bounded: on a timeout the
 // kernel records DPA_ERR_DEVICE_TIMEOUT and every role leaves its loop.
 #pragma once
+#include <climits>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -461,17 +462,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
         __syncthreads();
         if (warp == kLoadWarp) {
             const int each = a.E / 32 + 1, e0 = min(lane * each, a.E + 1), e1 = min(e0 + each, a.E + 1);
-            int sum = 0;
+            // 64 bits: offsets out of order name rows many times over (1024 groups of 2^30 rows, 2^33 tiles)
+            int64_t sum = 0;
             for (int e = e0; e < e1; ++e) sum += groups.pref[e];
-            int incl = sum;
+            int64_t incl = sum;
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            int before = incl - sum;
+            int64_t before = incl - sum;
             for (int e = e0; e < e1; ++e) {
                 const int c = groups.pref[e];
-                groups.pref[e] = before;
+                groups.pref[e] = static_cast<int>(min(before, static_cast<int64_t>(INT_MAX)));
                 before += c;
             }
         }
@@ -481,8 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinearArgs a, const
     if constexpr (CG == 2) cluster_sync();   // the pair's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    int ntiles = a.E > 0 ? groups.pref[a.E] * a.FT : a.ntiles;
-    if (S > 1 && ntiles > ncl) ntiles = ncl;   // one tile per cluster (only offsets out of order name more)
+    // grouped: as many as the offsets name, but no more than there can be when they are in order (with K
+    // split, one per cluster)
+    int ntiles = a.ntiles;
+    if (a.E > 0) ntiles = static_cast<int>(min(static_cast<int64_t>(groups.pref[a.E]) * a.FT, static_cast<int64_t>(ntiles)));
     // this CTA's K steps
     const int k0 = CG == 1 ? a.ksteps * rank / S : 0, k1 = CG == 1 ? a.ksteps * (rank + 1) / S : a.ksteps;
 

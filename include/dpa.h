@@ -504,7 +504,8 @@ dpa_status dpa_linear(const dpa_linear_desc* desc, const void* x, const void* w,
 /* The same product of each group's rows with that group's weights (device): rows
  * offsets[e] .. offsets[e+1] - 1 of x, residual and out belong to group e. offsets: int32
  * [n_groups + 1] on the device, ascending, as dpa_sort_pairs writes them (values outside [0, rows]
- * read as the nearest row). w, w_mul [n_groups][out_features][in_features]; bias, bias_mul
+ * read as the nearest row; out of order, nothing outside the buffers is touched, but which rows are
+ * written, and with which group, is not defined). w, w_mul [n_groups][out_features][in_features]; bias, bias_mul
  * [n_groups][out_features]. Rows behind the last group are neither used nor written; a group may
  * be empty. n_groups <= 1024. */
 dpa_status dpa_grouped_linear(const dpa_linear_desc* desc, int n_groups, const void* x, const int32_t* offsets,
