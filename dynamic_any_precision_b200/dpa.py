@@ -692,8 +692,11 @@ def dense_moe_forward(layer: DenseLayer, x, bufs, y=None, aux: Optional[dict] = 
     between the two products, every other intermediate is fp32. Returns y (int16 bf16 bits [T][H])."""
     import torch
     if stream is not None or x.get_device() != torch.cuda.current_device():
+        dev = _device(x)
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"stream: expected a stream of cuda:{dev}, got one of {stream.device}")
         # every buffer of the call, the router's outputs among them, belongs to the call's stream
-        with torch.cuda.device(_device(x)), torch.cuda.stream(stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
             return dense_moe_forward(layer, x, bufs, y, aux)
     ws = bufs["ws"]
     if y is None:

@@ -4,12 +4,14 @@ import os
 import subprocess
 import sys
 import threading
+import types
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from dynamic_any_precision_b200 import dpa  # noqa: E402
+from dynamic_any_precision_b200 import dpa, workloads as W  # noqa: E402
 from test_gpu_dense import DT, close, gen, normal, sorted_rows  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -191,3 +193,23 @@ def test_16_bit_outputs_of_very_long_sums(rows, N, dtype, gated):
         got = dpa.grouped_linear(x, off, w2, ws, w_mul=w2 if gated else None)
         close(got, ref, (part + torch.finfo(dt).eps / 2 * (1 + part)) * ref)
     assert dpa.device_status(ws) == 0
+
+
+# ---------------------------------------------------------------------------------- the layer
+
+def test_dense_layer_refuses_a_stream_of_another_device():
+    # it would run on the default stream of x's device, beside the work that the caller has ordered
+    shape = W.TINY
+    layer = dpa.DenseLayer.from_host(dpa.make_desc(shape), *W.all_expert_weights(shape), W.router_weights(shape))
+    x = torch.from_numpy(W.tokens(shape, 3).view(np.int16)).cuda()
+    y = torch.full_like(x, 5)
+    other = types.SimpleNamespace(device=torch.device("cuda", x.get_device() + 1), cuda_stream=0)
+    with pytest.raises(ValueError):
+        dpa.dense_moe_forward(layer, x, layer.buffers(3), y=y, stream=other)
+    torch.cuda.synchronize()
+    assert bool((y == 5).all())
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    got = dpa.dense_moe_forward(layer, x, layer.buffers(3), stream=stream)
+    stream.synchronize()
+    assert torch.equal(got, dpa.dense_moe_forward(layer, x, layer.buffers(3)))
