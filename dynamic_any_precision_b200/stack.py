@@ -78,12 +78,14 @@ class DenseStack:
     def forward(self, h, bufs, aux_per_layer=None, stream=None):
         """Run every layer on the residual stream h (fp32 [T][H], updated in place). aux_per_layer:
         optional list of aux dicts. Returns x, the normalised input the next layer would read."""
+        import torch
         x, y = bufs["x"], bufs["y"]
-        dpa.residual_rmsnorm(h, x, None, stream=stream)
-        for i, layer in enumerate(self.layers):
-            aux = aux_per_layer[i] if aux_per_layer is not None else None
-            dpa.dense_moe_forward(layer, x, bufs, y=y, aux=aux, stream=stream)
-            dpa.residual_rmsnorm(h, x, y, stream=stream)
+        with torch.cuda.device(h.device):   # the glue launches on the current device
+            dpa.residual_rmsnorm(h, x, None, stream=stream)
+            for i, layer in enumerate(self.layers):
+                aux = aux_per_layer[i] if aux_per_layer is not None else None
+                dpa.dense_moe_forward(layer, x, bufs, y=y, aux=aux, stream=stream)
+                dpa.residual_rmsnorm(h, x, y, stream=stream)
         return x
 
 
