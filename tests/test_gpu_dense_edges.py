@@ -1,5 +1,6 @@
 """Edges of the expert row sort, the row calls and the dense products that the sizes of the other tests
 pass by."""
+import math
 import os
 import subprocess
 import sys
@@ -193,6 +194,38 @@ def test_16_bit_outputs_of_very_long_sums(rows, N, dtype, gated):
         got = dpa.grouped_linear(x, off, w2, ws, w_mul=w2 if gated else None)
         close(got, ref, (part + torch.finfo(dt).eps / 2 * (1 + part)) * ref)
     assert dpa.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "gelu"])
+def test_activations_of_every_16_bit_value(act, dtype):
+    # One input of weight 1, so that the sum is the value itself. The exponential's argument comes from at
+    # most 5 roundings, 2^-24 of it each; the exponential, reciprocal, GELU's fit and the products around
+    # them add less than 2^-20 of the result. The reciprocal is 0 below 2^-126 (times v).
+    bits = torch.arange(-(1 << 15), 1 << 15, device="cuda").to(torch.int16).view(DT[dtype])
+    v = bits[torch.isfinite(bits)]
+    d = v.double()
+    if act == "silu":
+        arg, ref = d.abs(), d / (1 + torch.exp(-d))
+    elif act == "gelu_tanh":
+        arg = 2 * math.sqrt(2 / math.pi) * (d.abs() + 0.044715 * d.abs() ** 3)
+        ref = d / (1 + torch.exp(-torch.sign(d) * arg))
+    else:
+        arg, ref = d * d / 2, d * torch.special.erfc(-d * math.sqrt(0.5)) / 2
+    tol = ref.abs() * (5 * 2.0 ** -24 * arg + 2.0 ** -20) + d.abs() * 2.0 ** -126 + 2.0 ** -126
+    x = torch.zeros((v.numel(), 8), dtype=DT[dtype], device="cuda")
+    x[:, 3] = v
+    ws = dpa.new_linear_workspace()
+    for rows, n in ((v.numel(), 24), (4 * 37, 7)):    # whole 16-byte outputs, single ones
+        w = torch.zeros((n, 8), dtype=DT[dtype], device="cuda")
+        w[:, 3] = 1
+        for a in range(0, v.numel(), max(rows, v.numel() // 40)):
+            y = dpa.linear(x[a:a + rows], w, ws, act=act, out_dtype=torch.float32)
+            for f in (0, n - 1):
+                close(y[:, f], ref[a:a + rows], tol[a:a + rows])
+    few = torch.cat([dpa.linear(x[a:a + 16], w, ws, act=act, out_dtype=torch.float32)[:, 2]
+                     for a in range(0, v.numel(), 16)])    # the kernel for few rows
+    close(few, ref, tol)
 
 
 # ---------------------------------------------------------------------------------- the layer
