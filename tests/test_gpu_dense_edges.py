@@ -13,7 +13,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from dynamic_any_precision_b200 import dpa, workloads as W  # noqa: E402
-from test_gpu_dense import DT, close, gen, normal, sorted_rows  # noqa: E402
+from test_gpu_dense import DT, close, gen, host_sort, normal, rounding, routing, sorted_rows  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -118,7 +118,90 @@ def test_two_host_threads_launch_the_same_kernel_with_different_sizes():
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("T,K,E", [(9000, 4, 96), (300, 8, 1024), (70000, 2, 64)])
+def test_sorts_of_several_chunks_captured(T, K, E):
+    # two kernels, the second of which starts early: behind a kernel that writes the ids and in front of one
+    # that reads the places, all in one graph
+    ids = [torch.from_numpy(routing(T, K, E, s, 0.1)).cuda() for s in range(6)]
+    x = normal(gen(E), T, 64, dtype=torch.bfloat16)
+    source, idx, ws = ids[0].clone(), torch.empty_like(ids[0]), dpa.new_sort_workspace(T * K, E)
+    rows = torch.zeros((T * K, 64), dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        idx.copy_(source)
+        pos, order, offsets = dpa.sort_pairs(idx, E, ws)
+        dpa.permute_rows(x, pos, out=rows)
+        return pos, order, offsets, dpa.permute_rows_backward(rows, pos)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        pos, order, offsets, dx = step()
+    kept = []
+    with torch.cuda.stream(stream):
+        for i in ids[1:]:      # one replay right after another
+            source.copy_(i)
+            graph.replay()
+            kept.append([t.clone() for t in (pos, order, offsets, dx)])
+    torch.cuda.synchronize()
+    for i, got in zip(ids[1:], kept):
+        for a, b in zip(got, host_sort(i.cpu().numpy(), E)):
+            assert np.array_equal(a.cpu().numpy(), b)
+        routed = ((i >= 0) & (i < E)).sum(1, keepdim=True)
+        assert torch.equal(got[3], (x.float() * routed).bfloat16())    # up to 8 equal rows: exact in fp32
+
+
 # ------------------------------------------------------------------------------------- rows
+
+def sums_from_the_ring(T, H, bits):
+    """Whether a row sum of rows of `bits`-bit elements takes the kernels that stream rows through shared
+    memory: runs of 128 16-byte pieces per warp of 4 and round of 2 make 2 (whole pieces) or 4 (others)
+    blocks per SM (the launcher's rule, restated)."""
+    widest = 128 // bits
+    run, whole = 64 * widest, H % widest == 0
+    runs = T * ((H - 1) // run + 1) if whole else T * H // run
+    return runs // 8 >= (2 if whole else 4) * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+RING = [(1300, 3, 16, 2047, 0.3), (8000, 2, 8, 331, 0.2), (2500, 5, 16, 1036, 0.1), (40000, 1, 4, 63, 0.5),
+        (1200, 8, 64, 2048, 0.3), (3000, 4, 16, 520, 0.2), (2500, 2, 8, 8, 0.4), (700, 32, 64, 2056, 0.6)]
+
+
+@pytest.mark.parametrize("types", ["bf16-bf16", "fp16-fp16", "fp32-fp32", "bf16-fp32", "fp16-fp32", "fp32-bf16",
+                                   "fp32-fp16"])
+@pytest.mark.parametrize("T,K,E,H,drop", RING)
+def test_row_sums_through_the_ring(T, K, E, H, drop, types):
+    zt, yt = (DT[t] for t in types.split("-"))
+    assert sums_from_the_ring(T, H, zt.itemsize * 8)
+    _, pos, _, live = sorted_rows(T, K, E, drop, T + H)
+    pos[5:300] = -1        # tokens without pairs, one after another
+    g = gen(T * 3 + H)
+    z = normal(g, T * K, H, dtype=zt)
+    z[live:] = float("nan")
+    at = pos.clamp_min(0).long()
+    for wdt in (torch.float64, torch.float32, None):
+        w = None if wdt is None else torch.rand((T, K), generator=g, device="cuda").to(wdt)
+        ref, mag = (torch.zeros((T, H), dtype=torch.float64, device="cuda") for _ in range(2))
+        for k in range(K):
+            term = torch.where((pos[:, k] >= 0)[:, None], z[at[:, k]].double(), 0.0)
+            if w is not None:
+                term = term * w[:, k:k + 1].double()
+            ref += term
+            mag += term.abs()
+        if w is not None:
+            w = torch.where(pos >= 0, w, float("nan"))    # gates of unrouted pairs are not used
+        for res in (None, normal(g, T, H, dtype=yt), normal(g, T, H)):
+            r, m = (ref, mag) if res is None else (ref + res.double(), mag + res.double().abs())
+            y = dpa.unpermute_rows(z, pos, w, residual=res, out_dtype=yt)
+            # K products and K + 1 additions in fp32, gates rounded to fp32, one rounding to y
+            close(y, r, (K + 3) * 2.0 ** -24 * m + rounding(r, yt) * (1 + 2.0 ** -20))
+            if res is not None and res.dtype == yt:    # in place on the residual
+                h = res.clone()
+                assert dpa.unpermute_rows(z, pos, w, residual=h, out=h) is h and torch.equal(h, y)
+
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("T,K,H", [(9000, 2, 72), (40, 17, 515), (1500, 8, 2047), (33, 4, 4096), (5000, 1, 130)])
