@@ -119,10 +119,14 @@ cudaError_t launch_linear(const LinearArgs& in, bool f16, const void* x, const v
     int64_t clusters;
     // K blocks: the tensor cores drop the bits below the accumulator's last place at every step of 16
     // inputs, which takes about 1e-9 of the sum per input away (K = 8192: 9e-6; with a gate twice
-    // that). 16-bit outputs see it in very long sums only (long_sums). For fp32 outputs of more than 768 inputs (512 with an
-    // activation, 256 with a gate, which widen the error) blocks of 256 are added in fp32 with
-    // rounding: 3e-7 whatever K. The running sums take a third of tensor memory, so a tile has at most
-    // 160 tokens then.
+    // that). 16-bit outputs see it in very long sums only (long_sums). For fp32 outputs blocks of 256
+    // inputs are added in fp32 with rounding, from the length on where one accumulator's error would pass
+    // 1e-6 of the outputs (root mean squares over random terms): at 768 inputs 9.5e-7, with an activation
+    // at 512 7.7e-7 (it widens the error), with a gate at 256 6.4e-7. In blocks it is 3.4e-7 to 3.6e-7 up to
+    // 8192 inputs, with a gate 6.3e-7 to 6.9e-7 (an fp32 product by the library 4.9e-7 at 768, 1.6e-6 at
+    // 8192). Not from 256 on without a gate, for the running sums take time, and a third of tensor memory,
+    // so that a tile has at most 160 tokens: 4096x768x2048 23.7 us against 18.4, 4096x512x2048 20.3 against
+    // 16.9, the down products of 128 experts of 768 (2040 tokens) 122 against 95.
     const bool blocks =
         a.out32 ? a.ksteps > (gated ? 4 : a.act != DPA_ACT_NONE ? 8 : 12) : long_sums(a, gated);
     if (a.E > 0) {

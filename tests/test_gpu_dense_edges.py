@@ -252,6 +252,40 @@ def test_pairs_of_blocks_back_to_back():
                 assert torch.equal(y, ref)
 
 
+@pytest.mark.parametrize("rows,N", [(40, 96), (300, 520), (2000, 2500)])
+@pytest.mark.parametrize("border,act,gated", [(768, "none", False), (512, "relu", False), (256, "silu", True)])
+def test_fp32_outputs_around_the_length_where_blocks_begin(rows, N, border, act, gated):
+    # Positive terms. Up to the border one accumulator takes K / 16 steps, each off by at most two
+    # roundings or truncations, 2^-23 of the sum so far; behind it the blocks' sums (16 steps) are added with
+    # rounding. SiLU (slope at most 1.13) and the gate add their own errors once each, 2^-20 of the value.
+    g = gen(rows + border)
+    ws = dpa.new_linear_workspace()
+    off = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device="cuda")
+    errors = []
+    for K in (border, border + 64):
+        x = torch.rand((rows, K), generator=g, device="cuda").half()
+        w = (torch.rand((N, K), generator=g, device="cuda") * (8 / K)).half()
+        u = w.flip(0).contiguous() if gated else None
+        ref = x.double() @ w.double().T
+        steps = min(K, border) / 16 + 1
+        tol = 2 * steps * 2.0 ** -23 + (K / 256 + 16) * 2.0 ** -24
+        if act == "silu":
+            ref, tol = ref * torch.sigmoid(ref), 1.13 * tol + 2.0 ** -20
+        if gated:
+            ref, tol = ref * (x.double() @ u.double().T), 2 * tol + tol * tol
+        y = dpa.linear(x, w, ws, act=act, w_mul=u, out_dtype=torch.float32)
+        close(y, ref, tol * ref)
+        w2, u2 = torch.stack((w, w)), None if u is None else torch.stack((u, u))
+        z = dpa.grouped_linear(x, off, w2, ws, act=act, w_mul=u2, out_dtype=torch.float32)
+        close(z, ref, tol * ref)
+        errors.append([float(((t.double() - ref) / ref).abs().mean()) for t in (y, z)])
+    assert dpa.device_status(ws) == 0
+    # Two blocks or more against one accumulator: without blocks the longer sum would be the less exact one.
+    # (With fewer rows K is split over the CTAs of a cluster: 128 inputs per accumulator at either length.)
+    if border > 256 and rows == 2000:
+        assert errors[1][0] < errors[0][0] and errors[1][1] < errors[0][1], errors
+
+
 @pytest.mark.parametrize("rows,N,dtype", [(16, 400, "fp16"), (40, 40, "fp16"), (300, 200, "fp16"), (300, 200, "bf16"),
                                           (2560, 1024, "fp16")])
 @pytest.mark.parametrize("gated", [False, True])
