@@ -365,6 +365,8 @@ def residual_rmsnorm(h, x, y=None, stream=None):
 
 
 # ------------------------------------------------------------- dense experts: rows and products
+# These calls record no autograd history: their results never require gradients, whatever the inputs do.
+# The row calls' gradients are calls of their own; the products have none.
 
 _DTYPES = _FLOATS = None
 _current_device = _raw_stream = _empty_like = _empty_strided = None
@@ -461,8 +463,11 @@ def _like(t, stream):
         return _empty_like(t)
 
 
+# Sizes go to the library as 32-bit integers, and ctypes passes the low 32 bits of a larger one: the calls
+# below refuse those (DPA_ERR_UNSUPPORTED) before it could take them for small sizes.
+
 def sort_workspace_size(n_pairs: int, n_experts: int) -> int:
-    n = lib().dpa_sort_workspace_size(n_pairs, n_experts)
+    n = 0 if (n_pairs | n_experts) >> 31 else lib().dpa_sort_workspace_size(n_pairs, n_experts)
     if n == 0:
         raise DpaError(1, "dpa_sort_workspace_size")
     return n
@@ -488,6 +493,8 @@ def sort_pairs(idx, n_experts: int, ws, pos=None, order=None, offsets=None, stre
     [n_experts + 1]), int32: the place of each pair (-1 if not routed), the pair at each place
     (unrouted ones last), the places before each expert."""
     dev, P = _device(idx), idx.numel()
+    if (P | n_experts) >> 31:
+        raise DpaError(1 if n_experts < 0 else 2, "dpa_sort_pairs")
     ip = _arg(idx, "idx", idx.shape, "int32", dev)
     if pos is None:
         pos = _like(idx, stream)
@@ -515,6 +522,8 @@ def permute_rows(x, pos, out=None, stream=None):
     uninitialised)."""
     dev, code = _device(x), _float_type(x)
     (T, H), K = x.shape, pos.shape[-1]
+    if (T | K | H) >> 31:
+        raise DpaError(2, "dpa_permute_rows")
     xp, pp = _own(x, "x"), _arg(pos, "pos", (T, K), "int32", dev)
     if out is None:
         out = _new(x, (T * K, H), x.dtype, stream)
@@ -547,6 +556,8 @@ def unpermute_rows(z, pos, weights=None, residual=None, out=None, out_dtype=None
     weights: fp32 or fp64 [T][K] (None: all 1); residual: [T][H] of y's type or fp32, may be `out`.
     y has out_dtype (default: residual's, else z's): z's own type, or one of the two is fp32."""
     dev, (T, K), H = _device(z), pos.shape, z.shape[-1]
+    if (T | K | H) >> 31:
+        raise DpaError(2, "dpa_unpermute_rows")
     given, out = out is not None, _out(out, (T, H), z, residual, out_dtype, stream)
     code, zcode, wcode = _float_type(out), _float_type(z), _real(weights)
     rcode = code if residual is None else _float_type(residual)
@@ -573,6 +584,8 @@ def unpermute_rows_backward(dy, z, pos, weights, dz=None, dweights=None, stream=
     z's type; dz may be z. Rows of dz that no pair takes are left as they were (with dz=None: uninitialised);
     pairs that are not routed get dweights 0. The residual's gradient is dy itself."""
     dev, (T, K), H = _device(z), pos.shape, z.shape[-1]
+    if (T | K | H) >> 31:
+        raise DpaError(2, "dpa_unpermute_rows_backward")
     code, wcode = _float_type(z), _real(weights)
     if weights is None:
         raise ValueError("weights: expected a tensor")
@@ -599,6 +612,8 @@ def _product(fn, where, x, w, lead, groups, ws, bias, act, w_mul, bias_mul, resi
     """linear and grouped_linear: `lead` is () or (n_groups,), `groups` the group arguments of the
     call: () or (n_groups, offsets)."""
     dev, (rows, K), N = _device(x), x.shape, w.shape[-2]
+    if (rows | K | N | (lead[0] if lead else 0)) >> 31:
+        raise DpaError(2, where)
     wide, flat, rect = lead + (N, K), lead + (N,), (rows, N)
     given, out = out is not None, _out(out, rect, x, residual, out_dtype, stream)
     code, ocode = _float_type(x), _float_type(out)

@@ -345,6 +345,42 @@ def test_activations_of_every_16_bit_value(act, dtype):
     close(few, ref, tol)
 
 
+# ---------------------------------------------------------------------------------- refusals
+
+def test_sizes_past_32_bits_are_refused():
+    # their low 32 bits are small valid sizes; nothing of the tensors is touched
+    big = (1 << 32) + 8
+
+    def refused(call, *args, **kw):
+        with pytest.raises(dpa.DpaError) as err:
+            call(*args, **kw)
+        assert err.value.status == 2, err.value
+
+    with pytest.raises(dpa.DpaError):
+        dpa.sort_workspace_size(big, 8)
+    with pytest.raises(dpa.DpaError):
+        dpa.sort_workspace_size(8, big)
+    ws = dpa.new_sort_workspace(8, 8)
+    ids = torch.empty((big, 1), dtype=torch.int32, device="cuda")
+    refused(dpa.sort_pairs, ids, 8, ws)
+    offsets = ids.view(-1)
+    refused(dpa.sort_pairs, torch.zeros(8, dtype=torch.int32, device="cuda"), big - 1, ws, offsets=offsets)
+    with pytest.raises(dpa.DpaError) as err:
+        dpa.sort_pairs(torch.zeros(8, dtype=torch.int32, device="cuda"), -1, ws)
+    assert err.value.status == 1
+    rows = torch.empty((big, 1), dtype=torch.bfloat16, device="cuda")
+    refused(dpa.permute_rows, rows, ids, out=rows)
+    refused(dpa.unpermute_rows, rows, ids, out=rows)
+    refused(dpa.permute_rows_backward, rows, ids, dx=rows)
+    refused(dpa.unpermute_rows_backward, rows, rows, ids, ids.view(torch.float32), dz=rows, dweights=ids.view(torch.float32))
+    one = torch.zeros((1, 8), dtype=torch.bfloat16, device="cuda")
+    flat = rows.view(-1)
+    refused(dpa.linear, rows, one, ws, out=rows)                                   # rows
+    refused(dpa.linear, flat.view(1, big), flat.view(1, big), ws)                  # inputs
+    refused(dpa.linear, one[:, :1], rows, ws, out=flat.view(1, big))               # output features
+    refused(dpa.grouped_linear, one[:, :1], offsets, rows.view(big, 1, 1), ws)     # groups
+
+
 # ---------------------------------------------------------------------------------- the layer
 
 def test_dense_layer_refuses_a_stream_of_another_device():
