@@ -713,19 +713,25 @@ def dense_moe_forward(layer: DenseLayer, x, bufs, y=None, aux: Optional[dict] = 
         # every buffer of the call, the router's outputs among them, belongs to the call's stream
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             return dense_moe_forward(layer, x, bufs, y, aux)
-    ws = bufs["ws"]
+    # what the router reads is checked here, before the first launch
+    desc, dev, ws = layer.desc, _device(x), bufs["ws"]
+    _arg(x, "x", (len(x), desc.hidden), DTYPE_BF16, dev)
+    _arg(layer.w_router, "w_router", (desc.n_experts, desc.hidden), DTYPE_BF16, dev)
+    _workspace(ws, dev)
     if y is None:
         y = torch.empty(x.shape, dtype=torch.int16, device=x.device)
-    idx, gate = route(layer.desc, x, layer.w_router, ws)
+    else:
+        _arg(y, "y", x.shape, DTYPE_BF16, dev)
+    idx, gate = route(desc, x, layer.w_router, ws)
     if aux is not None:
         aux["topk_idx"], aux["topk_gate"] = idx, gate
     xb = x.view(torch.bfloat16)
     acc = None
-    for s in range(0 if layer.shared is None else layer.desc.n_shared):
+    for s in range(0 if layer.shared is None else desc.n_shared):
         g, u, d = (m[s] for m in layer.shared)
         linear(xb, g, ws, act="silu", w_mul=u, out=bufs["shared_h"])
         acc = linear(bufs["shared_h"], d, ws, residual=acc, out=bufs["shared_y"])
-    sort_pairs(idx, layer.desc.n_experts, bufs["sort_ws"], bufs["pos"], bufs["order"], bufs["offsets"])
+    sort_pairs(idx, desc.n_experts, bufs["sort_ws"], bufs["pos"], bufs["order"], bufs["offsets"])
     permute_rows(xb, bufs["pos"], out=bufs["rows"])
     grouped_linear(bufs["rows"], bufs["offsets"], layer.w_gate, ws, act="silu", w_mul=layer.w_up, out=bufs["h"])
     grouped_linear(bufs["h"], bufs["offsets"], layer.w_down, ws, out=bufs["z"])

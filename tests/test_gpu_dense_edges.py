@@ -399,3 +399,28 @@ def test_dense_layer_refuses_a_stream_of_another_device():
     got = dpa.dense_moe_forward(layer, x, layer.buffers(3), stream=stream)
     stream.synchronize()
     assert torch.equal(got, dpa.dense_moe_forward(layer, x, layer.buffers(3)))
+
+
+def test_dense_layer_checks_what_the_router_reads():
+    # a narrower x or router would be read past its end; nothing is launched
+    shape = W.TINY
+    desc = dpa.make_desc(shape)
+    weights, wr = W.all_expert_weights(shape), W.router_weights(shape)
+    layer = dpa.DenseLayer.from_host(desc, *weights, wr)
+    x = torch.from_numpy(W.tokens(shape, 4).view(np.int16)).cuda()
+    bufs = layer.buffers(4)
+    y = torch.full_like(x, 5)
+    wide = torch.zeros((4, 2 * shape.hidden), dtype=torch.int16, device="cuda")
+    for bad in (x[:, :-64].contiguous(), wide, wide[:, ::2], x.view(torch.float16), x.float(), x[0], x.cpu()):
+        with pytest.raises(ValueError):
+            dpa.dense_moe_forward(layer, bad, bufs, y=y)
+    for bad in (y[:3], y.float(), wide):
+        with pytest.raises(ValueError):
+            dpa.dense_moe_forward(layer, x, bufs, y=bad)
+    narrow = dpa.DenseLayer(desc, layer.w_gate, layer.w_up, layer.w_down, layer.w_router[:-1])
+    with pytest.raises(ValueError):
+        dpa.dense_moe_forward(narrow, x, bufs, y=y)
+    with pytest.raises(ValueError):
+        dpa.dense_moe_forward(layer, x, {**bufs, "ws": bufs["ws"].cpu()}, y=y)
+    torch.cuda.synchronize()
+    assert bool((y == 5).all())
