@@ -663,6 +663,8 @@ class DenseLayer:
     [S][inter][hidden], down [S][hidden][inter]), all bf16 or int16 bits."""
 
     def __init__(self, desc: LayerDesc, w_gate, w_up, w_down, w_router, shared=None):
+        if (0 if shared is None else len(shared[0])) != desc.n_shared:
+            raise ValueError(f"shared: expected the weights of {desc.n_shared} always-on experts")
         self.desc = desc
         self.w_gate, self.w_up, self.w_down, self.w_router, self.shared = w_gate, w_up, w_down, w_router, shared
 
@@ -727,7 +729,7 @@ def dense_moe_forward(layer: DenseLayer, x, bufs, y=None, aux: Optional[dict] = 
         aux["topk_idx"], aux["topk_gate"] = idx, gate
     xb = x.view(torch.bfloat16)
     acc = None
-    for s in range(0 if layer.shared is None else desc.n_shared):
+    for s in range(desc.n_shared):
         g, u, d = (m[s] for m in layer.shared)
         linear(xb, g, ws, act="silu", w_mul=u, out=bufs["shared_h"])
         acc = linear(bufs["shared_h"], d, ws, residual=acc, out=bufs["shared_y"])

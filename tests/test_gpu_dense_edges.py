@@ -424,3 +424,15 @@ def test_dense_layer_checks_what_the_router_reads():
         dpa.dense_moe_forward(layer, x, {**bufs, "ws": bufs["ws"].cpu()}, y=y)
     torch.cuda.synchronize()
     assert bool((y == 5).all())
+
+
+def test_dense_layer_wants_its_always_on_experts():
+    # without them the outputs would lack their part
+    shape = W.with_sizes(W.TINY, n_shared=2, name="two_shared")
+    weights, wr, shared = W.all_expert_weights(shape), W.router_weights(shape), W.shared_weights_bf16(shape)
+    desc = dpa.make_desc(shape)
+    for bad in (None, tuple(m[:1] for m in shared)):
+        with pytest.raises(ValueError):
+            dpa.DenseLayer.from_host(desc, *weights, wr, bad)
+    with pytest.raises(ValueError):
+        dpa.DenseLayer.from_host(dpa.make_desc(W.TINY), *W.all_expert_weights(W.TINY), wr, shared)
