@@ -71,8 +71,8 @@ int split_k(int64_t tiles, int ksteps) {
 // Rows per token tile, at most `most`, for pairs of CTAs: those for which the rounds of tiles over the
 // GPU's pairs take the least time, about rounds x (tile rows + 100).
 // Equal tiles of at most 256 alone leave pairs without work: 600x2048x4096 (48 tiles of 224 on 74 pairs)
-// 20.2 us, as 64 of 160 16.8; 2048x2048x1408 with a gate (two rounds of 256) 26.9, of 160 20.4;
-// 4819x1680x408 (one of 256) 21.8, of 160 17.0.
+// 16.3 us, as 64 of 160 13.7; 2048x2048x1408 with a gate (two rounds of 256) 27.2, of 160 21.3;
+// 4819x1680x408 (one of 256) 15.9, of 160 13.0.
 int pair_rows(int rows, int most, int FT, int pairs) {
     int best = 0;
     int64_t least = INT64_MAX;
@@ -91,7 +91,10 @@ int pair_rows(int rows, int most, int FT, int pairs) {
 // Whether the register kernel takes the call. Plain: up to 16 rows, and up to 32 where the weights are
 // small, so that start-up counts (32 rows: 2048x2816 6.6 us against 6.9 here; gated 10.4 against 8.3).
 // Grouped: up to 64 rows, 8 per group on average (8 tokens of top-8 through 128 experts of 2048x768
-// gated: 54 us against 62 here; 16 tokens 81 against 84, and the down products 50 against 47).
+// gated: 54 us against 62 here; 16 tokens 81 against 84, and the down products 50 against 47). The average
+// is over all groups, the empty ones included, for only the device knows the offsets: rows that all meet
+// in one group take turns of 8 (64 rows in one of 8 groups of 2048x768 gated: 21.4 us against 12.7; spread
+// over the 8 groups 8.5 against 11.9).
 bool few_rows(const LinearArgs& a, bool gated) {
     if (a.E > 0) return a.rows <= 64 && a.rows <= 8 * a.E;
     return a.rows <= 16 || (a.rows <= 32 && static_cast<int64_t>(a.K) * a.N * (gated ? 2 : 1) <= 1 << 23);
