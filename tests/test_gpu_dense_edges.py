@@ -13,7 +13,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from dynamic_any_precision_b200 import dpa, workloads as W  # noqa: E402
-from test_gpu_dense import DT, close, gen, host_sort, normal, rounding, routing, sorted_rows  # noqa: E402
+from test_gpu_dense import (DT, close, gen, host_sort, normal, product64, rounding, routing,  # noqa: E402
+                            sorted_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -116,6 +117,21 @@ def test_two_host_threads_launch_the_same_kernel_with_different_sizes():
             t.join()
         assert codes == [{0}, {0}]
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("P,E,drop", [(1048577, 64, 0.1), (1500003, 1000, 0.0), (3000001, 3, 0.5), (2097153, 1, 0.0)])
+def test_sorts_of_chunks_too_long_for_registers(P, E, drop):
+    idx = routing(P, 1, E, P, drop)
+    key = np.where((idx >= 0) & (idx < E), idx, E).reshape(-1)
+    order = np.argsort(key, kind="stable").astype(np.int32)
+    offsets = np.searchsorted(key[order], np.arange(E + 1)).astype(np.int32)
+    pos = np.full(P, -1, np.int32)
+    pos[order[:offsets[E]]] = np.arange(offsets[E])
+    ws = dpa.new_sort_workspace(P, E)
+    for _ in range(2):
+        got = dpa.sort_pairs(torch.from_numpy(idx).cuda(), E, ws)
+        for a, b in zip(got, (pos.reshape(P, 1), order, offsets)):
+            assert np.array_equal(a.cpu().numpy(), b)
 
 
 @pytest.mark.parametrize("T,K,E", [(9000, 4, 96), (300, 8, 1024), (70000, 2, 64)])
@@ -343,6 +359,34 @@ def test_activations_of_every_16_bit_value(act, dtype):
     few = torch.cat([dpa.linear(x[a:a + 16], w, ws, act=act, out_dtype=torch.float32)[:, 2]
                      for a in range(0, v.numel(), 16)])    # the kernel for few rows
     close(few, ref, tol)
+
+
+@pytest.mark.parametrize("first,counts,spare", [(5, [3, 0, 4], 2), (70, [40, 0, 90, 1], 130), (300, [700, 256, 0, 64], 1),
+                                                (1, [0, 0, 0], 40)])
+@pytest.mark.parametrize("N", [72, 1001])
+def test_grouped_rows_in_the_middle_of_the_tensor(first, counts, spare, N):
+    # rows before the first group and behind the last one are neither used nor written
+    K, E, live = 264, len(counts), sum(counts)
+    rows = first + live + spare
+    g = gen(rows + N)
+    x = normal(g, rows, K, dtype=torch.bfloat16)
+    x[:first] = float("nan")
+    x[first + live:] = float("nan")
+    w = normal(g, E, N, K, dtype=torch.bfloat16, scale=K ** -0.5)
+    offsets = torch.tensor([first] + [first + sum(counts[:e + 1]) for e in range(E)], dtype=torch.int32, device="cuda")
+    for odt in (torch.bfloat16, torch.float32):
+        y = torch.full((rows, N), 5.0, dtype=odt, device="cuda")
+        r = normal(g, rows, N, dtype=odt)
+        ws = dpa.new_linear_workspace()
+        dpa.grouped_linear(x, offsets, w, ws, act="relu", residual=r, out=y)
+        assert dpa.device_status(ws) == 0
+        assert bool((y[:first] == 5.0).all()) and bool((y[first + live:] == 5.0).all())
+        a = first
+        for e, n in enumerate(counts):
+            if n:
+                ref, tol = product64(x[a:a + n], w[e], None, "relu", None, None, r[a:a + n], odt)
+                close(y[a:a + n], ref, tol)
+            a += n
 
 
 # ---------------------------------------------------------------------------------- refusals
